@@ -331,6 +331,149 @@ hisa_status hisa_sparse_attention(const hisa_bf16 *q_att, const hisa_bf16 *k_att
                                   float *out, float *lse, hisa_stream_t stream);
 
 /*
+ * The 4-bit attention cache.  A token's key and value rows (HISA_ATT_DIM values each, the
+ * k_att and v_att of hisa_sparse_attention) take 144 bytes instead of 512:
+ *   kv4        uint8 [rows_k, HISA_KV4_ROW_BYTES]: 64 bytes of key nibbles, then 64 of
+ *              value nibbles; dimension d is the low (d even) or high nibble of byte d / 2.
+ *   kv4_scale  uint8 [rows_k, HISA_KV4_ROW_SCALES]: the scales of the 8 groups of
+ *              HISA_KV4_GROUP dimensions of the key, then of the value.  A scale byte b is
+ *              the fp16 number with the bit pattern b << 7 (5 exponent, 3 mantissa bits).
+ * A value is (nibble - 8) * scale; it is exact in bf16.  The row of a token is its key row
+ * (regions of cu_seqlens_k, as for the index keys).  kv4 and kv4_scale must be 16-byte
+ * aligned.
+ *
+ * hisa_kv4_store — quantise the rows of the query positions into the cache.
+ *   k_new, v_new   bf16 [total_q, HISA_ATT_DIM]: row r belongs to query row r, that is to
+ *                  the last q_len_s positions of every sequence: a whole prompt, a chunk of
+ *                  it, or the one token of a decode step.  The lengths count these tokens
+ *                  already (call it after hisa_append_keys or hisa_decode_step, which
+ *                  advance them); nothing else of the cache is touched.
+ * Per group of 16 dimensions with a = max |x|: scale = a / 7 rounded to nearest even (8-bit
+ * unsigned, 4 significant bits), at most 896; q = x / scale rounded to nearest even and
+ * clamped to -7..7.  An error is thus at most half a scale, except where |x| > 6720 or in
+ * groups with a below 2^-11, whose scales have fewer significant bits (below 7 * 2^-18
+ * they are zero).  A group that holds an infinity or a NaN reads back as NaN and raises
+ * HISA_ERR_INVALID_ARG in the device status word.
+ *
+ * hisa_kv4_load — the rows of the query positions back as bf16 (exactly the values that
+ * the attention uses), k_out and v_out bf16 [total_q, HISA_ATT_DIM].
+ *
+ * Both: a sequence with an unaligned region start or inconsistent lengths is skipped (its
+ * k_out and v_out rows are zeros) and reported in the device status word.
+ */
+#define HISA_KV4_GROUP 16
+#define HISA_KV4_ROW_BYTES 128
+#define HISA_KV4_ROW_SCALES 16
+hisa_status hisa_kv4_store(const hisa_bf16 *k_new, const hisa_bf16 *v_new,
+                           const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                           const int32_t *seqlens_k, int num_seqs, int total_q, uint8_t *kv4,
+                           uint8_t *kv4_scale, hisa_stream_t stream);
+
+hisa_status hisa_kv4_load(const uint8_t *kv4, const uint8_t *kv4_scale,
+                          const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                          const int32_t *seqlens_k, int num_seqs, int total_q, hisa_bf16 *k_out,
+                          hisa_bf16 *v_out, hisa_stream_t stream);
+
+/*
+ * hisa_sparse_attention_kv4 — hisa_sparse_attention over the 4-bit cache: the same scores,
+ * softmax and index rows, with k_att and v_att the values the cache stands for.
+ *
+ *   out (out)      bf16 [total_q, num_heads, HISA_ATT_DIM]; rows with no index are 0.
+ *   lse (out)      fp32 [total_q, num_heads] or NULL (then weights must be NULL too);
+ *                  -inf for a row with no index.
+ *   weights        int64 [rows_k] or NULL: the accumulated attention weight of every token,
+ *   (in/out)       in units of 2^-32.  The weight of each selected token, summed over the
+ *                  heads, is rounded to a whole unit and added; integer sums make the
+ *                  result independent of the order of the additions.  Not cleared here.
+ * Every other argument and the errors are those of hisa_sparse_attention.  out must be
+ * 16-byte aligned.
+ * Precision: q.k are sums of exact products in fp32 (a value of q more than 2^28 times
+ * smaller than its head's largest loses bits); maxima, sums, lse and weights are fp32;
+ * the softmax weights enter the value product as fp16 (11 significant bits) and the
+ * result is rounded once to bf16.
+ */
+hisa_status hisa_sparse_attention_kv4(const hisa_bf16 *q_att, const uint8_t *kv4,
+                                      const uint8_t *kv4_scale, const int32_t *topk_idx,
+                                      const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                      int num_seqs, int total_q, int num_heads, int k,
+                                      float scale, hisa_bf16 *out, float *lse, int64_t *weights,
+                                      hisa_stream_t stream);
+
+/*
+ * hisa_token_weights — the accumulated attention weight for the bf16 cache of
+ * hisa_sparse_attention:
+ *   weights[cu_seqlens_k[s] + j] += sum_h exp(scale * q_att[i][h] . k_att[j] - lse[i][h])
+ * over the entries j >= 0 of topk_idx[i], rounded to units of 2^-32 as above.
+ *   lse            fp32 [total_q, num_heads] as hisa_sparse_attention wrote it for the same
+ *                  q_att, k_att, topk_idx and scale; a head with lse -inf adds nothing.
+ * Any subset of the query rows may be given (an observation window at a prompt's end).
+ * A weight that is not a number, or larger than 4096, adds nothing and raises
+ * HISA_ERR_INVALID_ARG in the device status word, as does an index outside the region.
+ */
+hisa_status hisa_token_weights(const hisa_bf16 *q_att, const hisa_bf16 *k_att,
+                               const int32_t *topk_idx, const float *lse,
+                               const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                               int num_seqs, int total_q, int num_heads, int k, float scale,
+                               int64_t *weights, hisa_stream_t stream);
+
+/*
+ * hisa_evict_select — which tokens of every sequence stay in the cache.
+ *
+ *   weights        int64 [rows_k]: accumulated attention weights (above), or any other
+ *                  order of preference.
+ *   keep           int32 [num_seqs] (device): the budget of every sequence, >= 0.  A
+ *                  sequence of at most keep[s] tokens stays whole.
+ *   n_sink,        the first n_sink and the last n_recent positions stay before any other
+ *   n_recent       (cut to the budget, the first positions first); the rest of the budget
+ *                  goes to the largest weights, of equal ones to the lower position.
+ *   kept (out)     int32 [rows_k]: kept[cu_seqlens_k[s] + i] is the sequence-local position
+ *                  of the i-th token that stays, ascending; entries past the count are left
+ *                  as they were.
+ *   kept_len (out) int32 [num_seqs]: the count, min(len_s, keep[s]).
+ * A sequence with a negative budget, or with a length outside its region or above
+ * max_seqlen_k, gets kept_len -1 and raises HISA_ERR_INVALID_ARG in the device status word.
+ */
+hisa_status hisa_evict_select(const int64_t *weights, const int32_t *cu_seqlens_k,
+                              const int32_t *seqlens_k, const int32_t *keep, int num_seqs,
+                              int max_seqlen_k, int n_sink, int n_recent, int32_t *kept,
+                              int32_t *kept_len, hisa_stream_t stream);
+
+/*
+ * hisa_evict_rows — move the rows that stay to the front of their destination regions, for
+ * any set of row arrays at once (index keys, the 4-bit cache and its scales, bf16 keys and
+ * values, accumulated weights, original positions):
+ *   dst[cu_dst[s] + i] = src[cu_src[s] + kept[cu_src[s] + i]]     for i < kept_len[s]
+ *
+ *   arrays         host array of num_arrays (at most HISA_MAX_ROW_ARRAYS) descriptions, read
+ *                  before the call returns; row_bytes a multiple of 4, at most
+ *                  HISA_MAX_ROW_BYTES; src and dst 4-byte aligned (16 where the row size
+ *                  allows is faster).  dst == src moves in place; otherwise dst must not
+ *                  overlap any src, and no two dst may overlap.
+ *   cu_src, cu_dst int32 [num_seqs+1] regions of the sources and of the destinations; equal
+ *                  for arrays moved in place.
+ *   kept, kept_len as hisa_evict_select wrote them (kept strictly ascending per sequence);
+ *                  neither may be among the arrays.
+ *   max_keep       >= every kept_len (host copy, sizes the grid).
+ * Rows past kept_len[s] of a destination region are left as they were.  Afterwards
+ * kept_len is the new seqlens_k (with cu_dst as cu_seqlens_k), and hisa_pool_blocks renews
+ * the representatives.  Reported in the device status word: a kept_len that is negative,
+ * above max_keep or above its source region, a position outside the region (or, in place,
+ * one found to move a row backwards), in-place regions that differ
+ * (HISA_ERR_INVALID_ARG), a destination region that is too small (HISA_ERR_CAPACITY); the
+ * sequence (or the row) is not moved.  At most 65535 sequences.
+ */
+#define HISA_MAX_ROW_ARRAYS 8
+#define HISA_MAX_ROW_BYTES 4096
+typedef struct {
+  const void *src;
+  void *dst;
+  size_t row_bytes;
+} hisa_rows;
+hisa_status hisa_evict_rows(const hisa_rows *arrays, int num_arrays, const int32_t *cu_src,
+                            const int32_t *cu_dst, const int32_t *kept, const int32_t *kept_len,
+                            int num_seqs, int max_keep, hisa_stream_t stream);
+
+/*
  * hisa_device_status — wait for `stream`, then copy the sticky device status word
  * of the current device into *status (0 = no device-side error; otherwise the
  * OR of (1 << hisa_status) bits).  clear != 0 resets the word afterwards.

@@ -23,6 +23,12 @@ HISA_INDEX_DIM = 64
 HISA_BLOCK = 128
 HISA_MAX_M = 512
 HISA_MAX_TOPK = 2048
+HISA_KV4_GROUP = 16
+HISA_KV4_ROW_BYTES = 128
+HISA_KV4_ROW_SCALES = 16
+HISA_MAX_ROW_ARRAYS = 8
+HISA_MAX_ROW_BYTES = 4096
+HISA_WEIGHT_UNIT = 2.0 ** -32  # accumulated attention weights are whole multiples of this
 
 STATUS = {
     0: "HISA_OK",
@@ -58,6 +64,12 @@ EXPORTED = (
     "hisa_block_sparse_workspace_size",
     "hisa_test_fault",
     "hisa_decode_step",
+    "hisa_kv4_store",
+    "hisa_kv4_load",
+    "hisa_sparse_attention_kv4",
+    "hisa_token_weights",
+    "hisa_evict_select",
+    "hisa_evict_rows",
 )
 
 
@@ -109,6 +121,16 @@ def lib() -> ctypes.CDLL:
         L.hisa_decode_step.restype = I
         L.hisa_test_fault.argtypes = [I]
         L.hisa_test_fault.restype = I
+        L.hisa_kv4_store.argtypes = [P, P, P, P, P, I, I, P, P, P]
+        L.hisa_kv4_load.argtypes = [P, P, P, P, P, I, I, P, P, P]
+        L.hisa_sparse_attention_kv4.argtypes = [P, P, P, P, P, P, I, I, I, I, ctypes.c_float, P,
+                                                P, P, P]
+        L.hisa_token_weights.argtypes = [P, P, P, P, P, P, I, I, I, I, ctypes.c_float, P, P]
+        L.hisa_evict_select.argtypes = [P, P, P, P, I, I, I, I, P, P, P]
+        L.hisa_evict_rows.argtypes = [P, I, P, P, P, P, I, I, P]
+        for f in ("hisa_kv4_store", "hisa_kv4_load", "hisa_sparse_attention_kv4",
+                  "hisa_token_weights", "hisa_evict_select", "hisa_evict_rows"):
+            getattr(L, f).restype = I
         for f in ("hisa_pool_blocks", "hisa_append_keys", "hisa_select", "dsa_flat_select",
                   "hisa_device_status", "hisa_sparse_attention", "hisa_select_varm",
                   "hisa_fraction_blocks", "hisa_block_sparse_select"):
@@ -428,3 +450,216 @@ def hisa_sparse_attention(q_att: torch.Tensor, k_att: torch.Tensor, v_att: torch
                                        float(scale), _ptr(out), _ptr(lse), _stream(stream)),
            "hisa_sparse_attention")
     return out
+
+
+def _same_device(first: torch.Tensor, *rest) -> None:
+    """Every tensor on the current CUDA device: the library launches there."""
+    dev = first.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current device, got {dev}")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors are on {dev} and {t.device}")
+
+
+def _need_lengths(cu_q: Optional[torch.Tensor], cu_k: torch.Tensor,
+                  lens: Optional[torch.Tensor]) -> int:
+    """Number of sequences of the offsets and lengths, which have to agree on it."""
+    S = cu_k.numel() - 1
+    if S < 0 or (cu_q is not None and cu_q.numel() != S + 1) or \
+            (lens is not None and lens.numel() != S):
+        raise ValueError("cu_seqlens_q, cu_seqlens_k and seqlens_k disagree on the sequences")
+    return S
+
+
+def _need_kv4(kv4: torch.Tensor, kv4_scale: torch.Tensor):
+    _need(kv4, "kv4", torch.uint8, HISA_KV4_ROW_BYTES)
+    _need(kv4_scale, "kv4_scale", torch.uint8, HISA_KV4_ROW_SCALES)
+    if kv4.shape[0] != kv4_scale.shape[0]:
+        raise ValueError("kv4 and kv4_scale must have the same number of rows")
+
+
+def hisa_kv4_store(k_new: torch.Tensor, v_new: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                   cu_seqlens_k: torch.Tensor, seqlens_k: Optional[torch.Tensor],
+                   kv4: torch.Tensor, kv4_scale: torch.Tensor, stream=None) -> None:
+    """Quantise the key and value rows of the query positions (bf16 [total_q, 128]) into the
+    4-bit cache kv4 uint8 [rows, 128], kv4_scale uint8 [rows, 16]."""
+    _need(k_new, "k_new", torch.bfloat16, HISA_ATT_DIM)
+    _need(v_new, "v_new", torch.bfloat16, HISA_ATT_DIM)
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32)
+    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32)
+    _need(seqlens_k, "seqlens_k", torch.int32, optional=True)
+    _need_kv4(kv4, kv4_scale)
+    if v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must have the same shape")
+    S = _need_lengths(cu_seqlens_q, cu_seqlens_k, seqlens_k)
+    _same_device(kv4, kv4_scale, k_new, v_new, cu_seqlens_q, cu_seqlens_k, seqlens_k)
+    _check(lib().hisa_kv4_store(_ptr(k_new), _ptr(v_new), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
+                                _ptr(seqlens_k), S, k_new.shape[0], _ptr(kv4), _ptr(kv4_scale),
+                                _stream(stream)), "hisa_kv4_store")
+
+
+def hisa_kv4_load(kv4: torch.Tensor, kv4_scale: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                  cu_seqlens_k: torch.Tensor, seqlens_k: Optional[torch.Tensor], total_q: int,
+                  k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                  stream=None):
+    """The rows of the query positions back from the 4-bit cache; returns (k, v) bf16
+    [total_q, 128]."""
+    _need_kv4(kv4, kv4_scale)
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32)
+    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32)
+    _need(seqlens_k, "seqlens_k", torch.int32, optional=True)
+    if k_out is None:
+        k_out = torch.empty(total_q, HISA_ATT_DIM, dtype=torch.bfloat16, device=kv4.device)
+    if v_out is None:
+        v_out = torch.empty(total_q, HISA_ATT_DIM, dtype=torch.bfloat16, device=kv4.device)
+    _need(k_out, "k_out", torch.bfloat16, HISA_ATT_DIM)
+    _need(v_out, "v_out", torch.bfloat16, HISA_ATT_DIM)
+    if k_out.shape[0] != total_q or v_out.shape[0] != total_q:
+        raise ValueError("k_out and v_out need one row per query row")
+    S = _need_lengths(cu_seqlens_q, cu_seqlens_k, seqlens_k)
+    _same_device(kv4, kv4_scale, k_out, v_out, cu_seqlens_q, cu_seqlens_k, seqlens_k)
+    _check(lib().hisa_kv4_load(_ptr(kv4), _ptr(kv4_scale), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
+                               _ptr(seqlens_k), S, int(total_q), _ptr(k_out), _ptr(v_out),
+                               _stream(stream)), "hisa_kv4_load")
+    return k_out, v_out
+
+
+def _need_att(q_att: torch.Tensor, topk_idx: torch.Tensor, lse: Optional[torch.Tensor],
+              weights: Optional[torch.Tensor], rows: int):
+    """Checks shared by the attention over the 4-bit cache and the token weights."""
+    _need(q_att, "q_att", torch.bfloat16)
+    _need(topk_idx, "topk_idx", torch.int32)
+    _need(lse, "lse", torch.float32, optional=True)
+    _need(weights, "weights", torch.int64, optional=True)
+    if q_att.dim() != 3 or q_att.shape[2] != HISA_ATT_DIM:
+        raise ValueError(f"q_att must be [total_q, H, {HISA_ATT_DIM}], got {tuple(q_att.shape)}")
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != q_att.shape[0]:
+        raise ValueError("topk_idx must be [total_q, k]")
+    if lse is not None and lse.shape != q_att.shape[:2]:
+        raise ValueError("lse must be [total_q, H]")
+    if weights is not None and weights.numel() != rows:
+        raise ValueError("weights must hold one number per cache row")
+
+
+def hisa_sparse_attention_kv4(q_att: torch.Tensor, kv4: torch.Tensor, kv4_scale: torch.Tensor,
+                              topk_idx: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                              cu_seqlens_k: torch.Tensor, scale: float,
+                              out: Optional[torch.Tensor] = None,
+                              lse: Optional[torch.Tensor] = None,
+                              weights: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """Attention over each query's selected tokens of the 4-bit cache; returns out bf16
+    [total_q, H, 128].  weights int64 [rows], in units of HISA_WEIGHT_UNIT: the attention
+    weight of every selected token, summed over the heads, is added (needs lse)."""
+    _need_kv4(kv4, kv4_scale)
+    _need_att(q_att, topk_idx, lse, weights, kv4.shape[0])
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32)
+    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32)
+    S = _need_lengths(cu_seqlens_q, cu_seqlens_k, None)
+    if weights is not None and lse is None:
+        raise ValueError("weights need lse")
+    if out is None:
+        out = torch.empty(q_att.shape, dtype=torch.bfloat16, device=q_att.device)
+    _need(out, "out", torch.bfloat16)
+    if out.shape != q_att.shape:
+        raise ValueError("out must have the shape of q_att")
+    _same_device(kv4, kv4_scale, q_att, topk_idx, cu_seqlens_q, cu_seqlens_k, out, lse, weights)
+    _check(lib().hisa_sparse_attention_kv4(_ptr(q_att), _ptr(kv4), _ptr(kv4_scale),
+                                           _ptr(topk_idx), _ptr(cu_seqlens_q),
+                                           _ptr(cu_seqlens_k), S, q_att.shape[0], q_att.shape[1],
+                                           topk_idx.shape[1], float(scale), _ptr(out), _ptr(lse),
+                                           _ptr(weights), _stream(stream)),
+           "hisa_sparse_attention_kv4")
+    return out
+
+
+def hisa_token_weights(q_att: torch.Tensor, k_att: torch.Tensor, topk_idx: torch.Tensor,
+                       lse: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor,
+                       scale: float, weights: torch.Tensor, stream=None) -> torch.Tensor:
+    """Add the attention weight of every selected token of the bf16 cache, summed over the
+    heads, to weights int64 [rows] (units of HISA_WEIGHT_UNIT); returns weights."""
+    _need(k_att, "k_att", torch.bfloat16, HISA_ATT_DIM)
+    _need(lse, "lse", torch.float32)
+    _need(weights, "weights", torch.int64)
+    _need_att(q_att, topk_idx, lse, weights, k_att.shape[0])
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32)
+    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32)
+    S = _need_lengths(cu_seqlens_q, cu_seqlens_k, None)
+    _same_device(k_att, q_att, topk_idx, lse, cu_seqlens_q, cu_seqlens_k, weights)
+    _check(lib().hisa_token_weights(_ptr(q_att), _ptr(k_att), _ptr(topk_idx), _ptr(lse),
+                                    _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), S, q_att.shape[0],
+                                    q_att.shape[1], topk_idx.shape[1], float(scale),
+                                    _ptr(weights), _stream(stream)), "hisa_token_weights")
+    return weights
+
+
+def hisa_evict_select(weights: torch.Tensor, cu_seqlens_k: torch.Tensor,
+                      seqlens_k: Optional[torch.Tensor], keep: torch.Tensor, max_seqlen_k: int,
+                      n_sink: int, n_recent: int, kept: Optional[torch.Tensor] = None,
+                      kept_len: Optional[torch.Tensor] = None, stream=None):
+    """Which tokens of every sequence stay: the first n_sink, the last n_recent and those of
+    the largest weights, keep[s] in all; returns (kept int32 [rows], kept_len int32 [S])."""
+    _need(weights, "weights", torch.int64)
+    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32)
+    _need(seqlens_k, "seqlens_k", torch.int32, optional=True)
+    _need(keep, "keep", torch.int32)
+    S = _need_lengths(None, cu_seqlens_k, seqlens_k)
+    if keep.numel() != S:
+        raise ValueError("keep must hold one budget per sequence")
+    if kept is None:
+        kept = torch.empty(weights.numel(), dtype=torch.int32, device=weights.device)
+    if kept_len is None:
+        kept_len = torch.empty(S, dtype=torch.int32, device=weights.device)
+    _need(kept, "kept", torch.int32)
+    _need(kept_len, "kept_len", torch.int32)
+    if kept.numel() != weights.numel() or kept_len.numel() != S:
+        raise ValueError("kept must hold one number per cache row, kept_len one per sequence")
+    _same_device(weights, cu_seqlens_k, seqlens_k, keep, kept, kept_len)
+    _check(lib().hisa_evict_select(_ptr(weights), _ptr(cu_seqlens_k), _ptr(seqlens_k), _ptr(keep),
+                                   S, int(max_seqlen_k), int(n_sink), int(n_recent), _ptr(kept),
+                                   _ptr(kept_len), _stream(stream)), "hisa_evict_select")
+    return kept, kept_len
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p),
+                ("row_bytes", ctypes.c_size_t)]
+
+
+def hisa_evict_rows(src, dst, cu_src: torch.Tensor, cu_dst: torch.Tensor, kept: torch.Tensor,
+                    kept_len: torch.Tensor, max_keep: int, stream=None) -> None:
+    """Move the rows that stay (kept, kept_len of hisa_evict_select) of the row arrays src to
+    the front of their regions of the arrays dst; the same tensor in both moves in place."""
+    if len(src) != len(dst) or len(src) > HISA_MAX_ROW_ARRAYS:
+        raise ValueError(f"src and dst must be as many arrays, at most {HISA_MAX_ROW_ARRAYS}")
+    for name, t in (("cu_src", cu_src), ("cu_dst", cu_dst), ("kept", kept),
+                    ("kept_len", kept_len)):
+        _need(t, name, torch.int32)
+    S = _need_lengths(cu_dst, cu_src, kept_len)
+    _same_device(kept, kept_len, cu_src, cu_dst, *src, *dst)
+    rows = (_Rows * max(1, len(src)))()
+    spans = []
+    for i, (a, b) in enumerate(zip(src, dst)):
+        if a.dtype != b.dtype or a.dim() < 1 or a.shape[1:] != b.shape[1:]:
+            raise ValueError("a source and its destination must have rows of one type and shape")
+        if not a.is_contiguous() or not b.is_contiguous():
+            raise ValueError("row arrays must be contiguous")
+        if a.shape[0] != kept.numel():
+            raise ValueError("kept must hold one number per source row")
+        pa, pb = a.data_ptr(), b.data_ptr()
+        row = a.element_size()
+        for n in a.shape[1:]:
+            row *= n
+        rows[i] = _Rows(pa, pb, row)
+        in_place = pa == pb and a.shape == b.shape
+        spans.append((pa, pa + row * a.shape[0], pb, pb + row * b.shape[0], in_place))
+    for i, x in enumerate(spans):
+        for j, y in enumerate(spans):
+            if x[2] < y[1] and y[0] < x[3] and not (i == j and x[4]):
+                raise ValueError("a destination overlaps a source")
+            if i != j and x[2] < y[3] and y[2] < x[3]:
+                raise ValueError("two destinations overlap")
+    _check(lib().hisa_evict_rows(rows, len(src), _ptr(cu_src), _ptr(cu_dst), _ptr(kept),
+                                 _ptr(kept_len), S, int(max_keep), _stream(stream)),
+           "hisa_evict_rows")

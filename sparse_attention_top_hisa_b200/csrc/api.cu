@@ -54,6 +54,32 @@ cudaError_t launch_decode_select(const uint16_t *q, const uint16_t *k, const flo
                                  int *status, cudaStream_t st, uint16_t *append_kc = nullptr,
                                  float *append_reps = nullptr, int32_t *append_seqlens = nullptr,
                                  const uint16_t *new_keys = nullptr);
+cudaError_t launch_kv4_store(const uint16_t *k_new, const uint16_t *v_new, const int32_t *cu_q,
+                             const int32_t *cu_k, const int32_t *seqlens, int S, int total_q,
+                             uint8_t *kv4, uint8_t *kv4_scale, int *status, cudaStream_t st);
+cudaError_t launch_kv4_load(const uint8_t *kv4, const uint8_t *kv4_scale, const int32_t *cu_q,
+                            const int32_t *cu_k, const int32_t *seqlens, int S, int total_q,
+                            uint16_t *k_out, uint16_t *v_out, int *status, cudaStream_t st);
+cudaError_t launch_attention_kv4(const uint16_t *q, const uint8_t *kv4, const uint8_t *kv4_scale,
+                                 const int32_t *idx, const int32_t *cu_q, const int32_t *cu_k,
+                                 int S, int total_q, int H, int topk, float scale, uint16_t *out,
+                                 float *lse, int num_sms, int *status, cudaStream_t st);
+cudaError_t launch_token_weights(const uint16_t *q, const uint16_t *k, const int32_t *idx,
+                                 const float *lse, const int32_t *cu_q, const int32_t *cu_k, int S,
+                                 int total_q, int H, int topk, float scale, int64_t *weights,
+                                 int num_sms, int *status, cudaStream_t st);
+cudaError_t launch_token_weights_kv4(const uint16_t *q, const uint8_t *kv4,
+                                     const uint8_t *kv4_scale, const int32_t *idx,
+                                     const float *lse, const int32_t *cu_q, const int32_t *cu_k,
+                                     int S, int total_q, int H, int topk, float scale,
+                                     int64_t *weights, int num_sms, int *status, cudaStream_t st);
+cudaError_t launch_evict_select(const int64_t *weights, const int32_t *cu_k,
+                                const int32_t *seqlens, const int32_t *keep, int S,
+                                int max_seqlen_k, int n_sink, int n_recent, int32_t *kept,
+                                int32_t *kept_len, int *status, cudaStream_t st);
+cudaError_t launch_evict_rows(const hisa_rows *arrays, int n, const int32_t *cu_src,
+                              const int32_t *cu_dst, const int32_t *kept, const int32_t *kept_len,
+                              int S, int max_keep, int num_sms, int *status, cudaStream_t st);
 }  // namespace hisa
 
 using namespace hisa;
@@ -68,7 +94,8 @@ const char *kKindNames[K_NUM_KINDS] = {
     "token_score_split",  "token_select_scratch", "key_norm",      "dsa_filter",
     "dsa_select",         "dsa_fallback",         "inv_lists",      "inv_scan",
     "token_score_tc",     "reps_split",          "block_score_tc",  "decode_select",  "sparse_attention",
-    "expand_blocks",      "fraction_budget"};
+    "expand_blocks",      "fraction_budget",      "kv4_store",      "kv4_load",
+    "sparse_attention_kv4", "token_weights",      "evict_select",   "evict_rows"};
 std::atomic<long long> g_launches[K_NUM_KINDS];
 double g_ms[K_NUM_KINDS];
 long long g_timed[K_NUM_KINDS];
@@ -487,6 +514,138 @@ hisa_status hisa_sparse_attention(const hisa_bf16 *q_att, const hisa_bf16 *k_att
                                            cu_seqlens_k, num_seqs, total_q, num_heads, k, scale,
                                            out, lse, num_sms(), st,
                                            static_cast<cudaStream_t>(stream)));
+}
+
+hisa_status hisa_kv4_store(const hisa_bf16 *k_new, const hisa_bf16 *v_new,
+                           const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                           const int32_t *seqlens_k, int num_seqs, int total_q, uint8_t *kv4,
+                           uint8_t *kv4_scale, hisa_stream_t stream) {
+  if (num_seqs < 0 || total_q < 0) return HISA_ERR_INVALID_ARG;
+  if (total_q == 0) return HISA_OK;
+  if (num_seqs == 0 || !k_new || !v_new || !cu_seqlens_q || !cu_seqlens_k || !kv4 || !kv4_scale)
+    return HISA_ERR_INVALID_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(cu_seqlens_q, 4) ||
+      !aligned(cu_seqlens_k, 4) || !aligned(seqlens_k, 4) || !aligned(kv4, 16) ||
+      !aligned(kv4_scale, 16))
+    return HISA_ERR_UNALIGNED;
+  int *st = status_word();
+  if (!st) return HISA_ERR_CUDA;
+  return from_cuda(launch_kv4_store(k_new, v_new, cu_seqlens_q, cu_seqlens_k, seqlens_k, num_seqs,
+                                    total_q, kv4, kv4_scale, st,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+hisa_status hisa_kv4_load(const uint8_t *kv4, const uint8_t *kv4_scale,
+                          const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                          const int32_t *seqlens_k, int num_seqs, int total_q, hisa_bf16 *k_out,
+                          hisa_bf16 *v_out, hisa_stream_t stream) {
+  if (num_seqs < 0 || total_q < 0) return HISA_ERR_INVALID_ARG;
+  if (total_q == 0) return HISA_OK;
+  if (num_seqs == 0 || !k_out || !v_out || !cu_seqlens_q || !cu_seqlens_k || !kv4 || !kv4_scale)
+    return HISA_ERR_INVALID_ARG;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(cu_seqlens_q, 4) ||
+      !aligned(cu_seqlens_k, 4) || !aligned(seqlens_k, 4) || !aligned(kv4, 16) ||
+      !aligned(kv4_scale, 16))
+    return HISA_ERR_UNALIGNED;
+  int *st = status_word();
+  if (!st) return HISA_ERR_CUDA;
+  return from_cuda(launch_kv4_load(kv4, kv4_scale, cu_seqlens_q, cu_seqlens_k, seqlens_k,
+                                   num_seqs, total_q, k_out, v_out, st,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+hisa_status hisa_sparse_attention_kv4(const hisa_bf16 *q_att, const uint8_t *kv4,
+                                      const uint8_t *kv4_scale, const int32_t *topk_idx,
+                                      const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                      int num_seqs, int total_q, int num_heads, int k,
+                                      float scale, hisa_bf16 *out, float *lse, int64_t *weights,
+                                      hisa_stream_t stream) {
+  if (num_heads < 1 || num_heads > HISA_ATT_MAX_HEADS || k < 1 || num_seqs < 0 || total_q < 0 ||
+      !(scale == scale))
+    return HISA_ERR_INVALID_ARG;
+  if (total_q == 0) return HISA_OK;
+  if (num_seqs == 0 || total_q >= (1 << 25)) return HISA_ERR_INVALID_ARG;
+  if (!q_att || !kv4 || !kv4_scale || !topk_idx || !cu_seqlens_q || !cu_seqlens_k || !out ||
+      (weights && !lse))
+    return HISA_ERR_INVALID_ARG;
+  if (!aligned(q_att, 16) || !aligned(kv4, 16) || !aligned(kv4_scale, 16) ||
+      !aligned(topk_idx, 4) || !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4) ||
+      !aligned(out, 16) || !aligned(lse, 4) || !aligned(weights, 8))
+    return HISA_ERR_UNALIGNED;
+  int *st = status_word();
+  if (!st) return HISA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_attention_kv4(q_att, kv4, kv4_scale, topk_idx, cu_seqlens_q, cu_seqlens_k,
+                                       num_seqs, total_q, num_heads, k, scale, out, lse, num_sms(),
+                                       st, s);
+  if (e == cudaSuccess && weights)
+    e = launch_token_weights_kv4(q_att, kv4, kv4_scale, topk_idx, lse, cu_seqlens_q, cu_seqlens_k,
+                                 num_seqs, total_q, num_heads, k, scale, weights, num_sms(), st, s);
+  return from_cuda(e);
+}
+
+hisa_status hisa_token_weights(const hisa_bf16 *q_att, const hisa_bf16 *k_att,
+                               const int32_t *topk_idx, const float *lse,
+                               const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                               int num_seqs, int total_q, int num_heads, int k, float scale,
+                               int64_t *weights, hisa_stream_t stream) {
+  if (num_heads < 1 || num_heads > HISA_ATT_MAX_HEADS || k < 1 || num_seqs < 0 || total_q < 0 ||
+      !(scale == scale))
+    return HISA_ERR_INVALID_ARG;
+  if (total_q == 0) return HISA_OK;
+  if (num_seqs == 0 || total_q >= (1 << 25)) return HISA_ERR_INVALID_ARG;
+  if (!q_att || !k_att || !topk_idx || !lse || !cu_seqlens_q || !cu_seqlens_k || !weights)
+    return HISA_ERR_INVALID_ARG;
+  if (!aligned(q_att, 16) || !aligned(k_att, 16) || !aligned(topk_idx, 4) || !aligned(lse, 4) ||
+      !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4) || !aligned(weights, 8))
+    return HISA_ERR_UNALIGNED;
+  int *st = status_word();
+  if (!st) return HISA_ERR_CUDA;
+  return from_cuda(launch_token_weights(q_att, k_att, topk_idx, lse, cu_seqlens_q, cu_seqlens_k,
+                                        num_seqs, total_q, num_heads, k, scale, weights,
+                                        num_sms(), st, static_cast<cudaStream_t>(stream)));
+}
+
+hisa_status hisa_evict_select(const int64_t *weights, const int32_t *cu_seqlens_k,
+                              const int32_t *seqlens_k, const int32_t *keep, int num_seqs,
+                              int max_seqlen_k, int n_sink, int n_recent, int32_t *kept,
+                              int32_t *kept_len, hisa_stream_t stream) {
+  if (num_seqs < 0 || max_seqlen_k < 0 || n_sink < 0 || n_recent < 0) return HISA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return HISA_OK;
+  if (!weights || !cu_seqlens_k || !keep || !kept || !kept_len) return HISA_ERR_INVALID_ARG;
+  if (!aligned(weights, 8) || !aligned(cu_seqlens_k, 4) || !aligned(seqlens_k, 4) ||
+      !aligned(keep, 4) || !aligned(kept, 4) || !aligned(kept_len, 4))
+    return HISA_ERR_UNALIGNED;
+  int *st = status_word();
+  if (!st) return HISA_ERR_CUDA;
+  return from_cuda(launch_evict_select(weights, cu_seqlens_k, seqlens_k, keep, num_seqs,
+                                       max_seqlen_k, n_sink, n_recent, kept, kept_len, st,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+hisa_status hisa_evict_rows(const hisa_rows *arrays, int num_arrays, const int32_t *cu_src,
+                            const int32_t *cu_dst, const int32_t *kept, const int32_t *kept_len,
+                            int num_seqs, int max_keep, hisa_stream_t stream) {
+  if (num_arrays < 0 || num_arrays > HISA_MAX_ROW_ARRAYS || num_seqs < 0 || num_seqs > 65535 ||
+      max_keep < 0)
+    return HISA_ERR_INVALID_ARG;
+  if (num_arrays == 0 || num_seqs == 0 || max_keep == 0) return HISA_OK;
+  if (!arrays || !cu_src || !cu_dst || !kept || !kept_len) return HISA_ERR_INVALID_ARG;
+  for (int i = 0; i < num_arrays; i++) {
+    const hisa_rows &r = arrays[i];
+    if (!r.src || !r.dst || r.row_bytes < 4 || r.row_bytes > HISA_MAX_ROW_BYTES ||
+        r.row_bytes % 4 != 0)
+      return HISA_ERR_INVALID_ARG;
+    if (!aligned(r.src, 4) || !aligned(r.dst, 4)) return HISA_ERR_UNALIGNED;
+    for (int j = 0; j < num_arrays; j++)
+      if (j != i && r.dst == arrays[j].dst) return HISA_ERR_INVALID_ARG;
+  }
+  if (!aligned(cu_src, 4) || !aligned(cu_dst, 4) || !aligned(kept, 4) || !aligned(kept_len, 4))
+    return HISA_ERR_UNALIGNED;
+  int *st = status_word();
+  if (!st) return HISA_ERR_CUDA;
+  return from_cuda(launch_evict_rows(arrays, num_arrays, cu_src, cu_dst, kept, kept_len, num_seqs,
+                                     max_keep, num_sms(), st, static_cast<cudaStream_t>(stream)));
 }
 
 hisa_status hisa_timing_enable(int on) {

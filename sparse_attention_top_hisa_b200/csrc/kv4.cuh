@@ -1,0 +1,77 @@
+// The 4-bit cache format and the register-level pieces its readers share.
+//
+// A group of 16 dimensions shares a scale s; a value is q * s with a whole q of -7..7
+// stored as the nibble u = q + 8, low nibble first.  s is an unsigned e5m3 number kept
+// in one byte: bits 14..7 of its fp16 pattern.  s has 4 significant bits and q has 3, so
+// q * s is exact in fp16 and in bf16.
+//
+// Four bits per value were taken as whole numbers rather than as a 4-bit float (e2m1)
+// because their error on Gaussian rows is smaller at this group size (about 8.5% rms of
+// a value's spread against 10.5%) and because a nibble turns into an fp16 pair with one
+// logic operation and one FMA (below), where the float needs its sign moved apart.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace hisa {
+
+constexpr int KV4_DIM = HISA_ATT_DIM;              // 128
+constexpr int KV4_HALF = KV4_DIM / 2;              // bytes of a key's (or value's) nibbles
+constexpr int KV4_ROW = HISA_KV4_ROW_BYTES;        // key nibbles, then value nibbles
+constexpr int KV4_NS = HISA_KV4_ROW_SCALES;        // scale bytes of a row: 8 key, 8 value
+constexpr int KV4_GROUP = HISA_KV4_GROUP;          // 16
+static_assert(KV4_DIM == 128 && KV4_GROUP == 16 && KV4_ROW == 128 && KV4_NS == 16,
+              "the fragment layouts below take these sizes");
+
+__device__ __forceinline__ __half2 as_half2(uint32_t w) {
+  return *reinterpret_cast<const __half2 *>(&w);
+}
+__device__ __forceinline__ uint32_t as_u32(__half2 h) {
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Nibbles at bits 4..7 of both halves of w as fp16 values times the scale pair s:
+// 0x5400 is 64 and its low mantissa bit 1/16, so or-ing the nibble into bits 4..7 gives
+// 64 + u, and (64 + u) * s - 72 * s = (u - 8) * s, rounded once and exact.
+// c72 = -72 * s (72 has 4 significant bits, so it is exact too, and finite: s <= 896).
+__device__ __forceinline__ uint32_t kv4_pair(uint32_t w, __half2 s, __half2 c72) {
+  const uint32_t t = (w & 0x00F000F0u) | 0x54005400u;
+  return as_u32(__hfma2(as_half2(t), s, c72));
+}
+
+__device__ __forceinline__ __half2 kv4_c72(__half2 s) {
+  return __hmul2(s, as_half2(0xD480D480u));  // -72
+}
+
+// D += A (16 x 16, row) * B (16 x 8, col), fp16 in, fp32 out.  The matrix instruction
+// whose operands are registers: the 4-bit rows are turned into fragments where they are
+// used, where the one that reads shared memory would need every row written back there in
+// 16 bits (4x the bytes that arrived) before it could start.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 2^x (the hardware approximation: relative error about 2^-22, 2^-inf = 0)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+}  // namespace hisa

@@ -27,6 +27,12 @@ enum KernelKind {
   K_SPARSE_ATTENTION,
   K_EXPAND_BLOCKS,
   K_FRACTION_BUDGET,
+  K_KV4_STORE,
+  K_KV4_LOAD,
+  K_ATTENTION_KV4,
+  K_TOKEN_WEIGHTS,
+  K_EVICT_SELECT,
+  K_EVICT_ROWS,
   K_NUM_KINDS
 };
 
