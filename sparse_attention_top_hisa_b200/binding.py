@@ -452,18 +452,36 @@ def hisa_sparse_attention(q_att: torch.Tensor, k_att: torch.Tensor, v_att: torch
     return out
 
 
-def _same_device(first: torch.Tensor, *rest) -> None:
-    """Every tensor on the current CUDA device: the library launches there."""
-    dev = first.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current device, got {dev}")
-    for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors are on {dev} and {t.device}")
+# The entry points below are called once per layer and decode step, so their checks are
+# written to cost little on the host: one helper checks a tensor and gives its address,
+# and only a tensor that fails is looked at again to say why.
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """Index of the CUDA device of t, which has to be the current one."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current device, is on {t.device}")
+    return dev
 
 
-def _need_lengths(cu_q: Optional[torch.Tensor], cu_k: torch.Tensor,
-                  lens: Optional[torch.Tensor]) -> int:
+def _at(t: torch.Tensor, name: str, dtype, dev: int, cols: Optional[int] = None) -> int:
+    """Address of a tensor that is checked for device, dtype, contiguity and width."""
+    if t is None or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or \
+            (cols is not None and (t.dim() != 2 or t.shape[1] != cols)):
+        _need(t, name, dtype, cols)
+        raise ValueError(f"tensors must be on one device: {name} is on {t.device}")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _seqs(cu_q: Optional[torch.Tensor], cu_k: torch.Tensor, lens: Optional[torch.Tensor]) -> int:
     """Number of sequences of the offsets and lengths, which have to agree on it."""
     S = cu_k.numel() - 1
     if S < 0 or (cu_q is not None and cu_q.numel() != S + 1) or \
@@ -472,31 +490,26 @@ def _need_lengths(cu_q: Optional[torch.Tensor], cu_k: torch.Tensor,
     return S
 
 
-def _need_kv4(kv4: torch.Tensor, kv4_scale: torch.Tensor):
-    _need(kv4, "kv4", torch.uint8, HISA_KV4_ROW_BYTES)
-    _need(kv4_scale, "kv4_scale", torch.uint8, HISA_KV4_ROW_SCALES)
-    if kv4.shape[0] != kv4_scale.shape[0]:
-        raise ValueError("kv4 and kv4_scale must have the same number of rows")
-
-
 def hisa_kv4_store(k_new: torch.Tensor, v_new: torch.Tensor, cu_seqlens_q: torch.Tensor,
                    cu_seqlens_k: torch.Tensor, seqlens_k: Optional[torch.Tensor],
                    kv4: torch.Tensor, kv4_scale: torch.Tensor, stream=None) -> None:
     """Quantise the key and value rows of the query positions (bf16 [total_q, 128]) into the
     4-bit cache kv4 uint8 [rows, 128], kv4_scale uint8 [rows, 16]."""
-    _need(k_new, "k_new", torch.bfloat16, HISA_ATT_DIM)
-    _need(v_new, "v_new", torch.bfloat16, HISA_ATT_DIM)
-    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32)
-    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32)
-    _need(seqlens_k, "seqlens_k", torch.int32, optional=True)
-    _need_kv4(kv4, kv4_scale)
-    if v_new.shape != k_new.shape:
+    dev, i32 = _device_of(kv4, "kv4"), torch.int32
+    a = _at(kv4, "kv4", torch.uint8, dev, HISA_KV4_ROW_BYTES)
+    b = _at(kv4_scale, "kv4_scale", torch.uint8, dev, HISA_KV4_ROW_SCALES)
+    k = _at(k_new, "k_new", torch.bfloat16, dev, HISA_ATT_DIM)
+    v = _at(v_new, "v_new", torch.bfloat16, dev, HISA_ATT_DIM)
+    cq = _at(cu_seqlens_q, "cu_seqlens_q", i32, dev)
+    ck = _at(cu_seqlens_k, "cu_seqlens_k", i32, dev)
+    n = None if seqlens_k is None else _at(seqlens_k, "seqlens_k", i32, dev)
+    S, total_q = _seqs(cu_seqlens_q, cu_seqlens_k, seqlens_k), k_new.shape[0]
+    if v_new.shape[0] != total_q:
         raise ValueError("k_new and v_new must have the same shape")
-    S = _need_lengths(cu_seqlens_q, cu_seqlens_k, seqlens_k)
-    _same_device(kv4, kv4_scale, k_new, v_new, cu_seqlens_q, cu_seqlens_k, seqlens_k)
-    _check(lib().hisa_kv4_store(_ptr(k_new), _ptr(v_new), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
-                                _ptr(seqlens_k), S, k_new.shape[0], _ptr(kv4), _ptr(kv4_scale),
-                                _stream(stream)), "hisa_kv4_store")
+    if kv4.shape[0] != kv4_scale.shape[0]:
+        raise ValueError("kv4 and kv4_scale must have the same number of rows")
+    _check(lib().hisa_kv4_store(k, v, cq, ck, n, S, total_q, a, b, _raw_stream(stream, dev)),
+           "hisa_kv4_store")
 
 
 def hisa_kv4_load(kv4: torch.Tensor, kv4_scale: torch.Tensor, cu_seqlens_q: torch.Tensor,
@@ -505,41 +518,41 @@ def hisa_kv4_load(kv4: torch.Tensor, kv4_scale: torch.Tensor, cu_seqlens_q: torc
                   stream=None):
     """The rows of the query positions back from the 4-bit cache; returns (k, v) bf16
     [total_q, 128]."""
-    _need_kv4(kv4, kv4_scale)
-    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32)
-    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32)
-    _need(seqlens_k, "seqlens_k", torch.int32, optional=True)
+    dev, i32 = _device_of(kv4, "kv4"), torch.int32
+    a = _at(kv4, "kv4", torch.uint8, dev, HISA_KV4_ROW_BYTES)
+    b = _at(kv4_scale, "kv4_scale", torch.uint8, dev, HISA_KV4_ROW_SCALES)
+    cq = _at(cu_seqlens_q, "cu_seqlens_q", i32, dev)
+    ck = _at(cu_seqlens_k, "cu_seqlens_k", i32, dev)
+    n = None if seqlens_k is None else _at(seqlens_k, "seqlens_k", i32, dev)
+    S = _seqs(cu_seqlens_q, cu_seqlens_k, seqlens_k)
     if k_out is None:
-        k_out = torch.empty(total_q, HISA_ATT_DIM, dtype=torch.bfloat16, device=kv4.device)
+        k_out = torch.empty((total_q, HISA_ATT_DIM), dtype=torch.bfloat16, device=kv4.device)
     if v_out is None:
-        v_out = torch.empty(total_q, HISA_ATT_DIM, dtype=torch.bfloat16, device=kv4.device)
-    _need(k_out, "k_out", torch.bfloat16, HISA_ATT_DIM)
-    _need(v_out, "v_out", torch.bfloat16, HISA_ATT_DIM)
+        v_out = torch.empty((total_q, HISA_ATT_DIM), dtype=torch.bfloat16, device=kv4.device)
+    k = _at(k_out, "k_out", torch.bfloat16, dev, HISA_ATT_DIM)
+    v = _at(v_out, "v_out", torch.bfloat16, dev, HISA_ATT_DIM)
     if k_out.shape[0] != total_q or v_out.shape[0] != total_q:
         raise ValueError("k_out and v_out need one row per query row")
-    S = _need_lengths(cu_seqlens_q, cu_seqlens_k, seqlens_k)
-    _same_device(kv4, kv4_scale, k_out, v_out, cu_seqlens_q, cu_seqlens_k, seqlens_k)
-    _check(lib().hisa_kv4_load(_ptr(kv4), _ptr(kv4_scale), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
-                               _ptr(seqlens_k), S, int(total_q), _ptr(k_out), _ptr(v_out),
-                               _stream(stream)), "hisa_kv4_load")
+    if kv4.shape[0] != kv4_scale.shape[0]:
+        raise ValueError("kv4 and kv4_scale must have the same number of rows")
+    _check(lib().hisa_kv4_load(a, b, cq, ck, n, S, int(total_q), k, v, _raw_stream(stream, dev)),
+           "hisa_kv4_load")
     return k_out, v_out
 
 
-def _need_att(q_att: torch.Tensor, topk_idx: torch.Tensor, lse: Optional[torch.Tensor],
-              weights: Optional[torch.Tensor], rows: int):
-    """Checks shared by the attention over the 4-bit cache and the token weights."""
-    _need(q_att, "q_att", torch.bfloat16)
-    _need(topk_idx, "topk_idx", torch.int32)
-    _need(lse, "lse", torch.float32, optional=True)
-    _need(weights, "weights", torch.int64, optional=True)
-    if q_att.dim() != 3 or q_att.shape[2] != HISA_ATT_DIM:
-        raise ValueError(f"q_att must be [total_q, H, {HISA_ATT_DIM}], got {tuple(q_att.shape)}")
-    if topk_idx.dim() != 2 or topk_idx.shape[0] != q_att.shape[0]:
+def _att_shapes(q_att: torch.Tensor, topk_idx: torch.Tensor, lse: Optional[torch.Tensor],
+                weights: Optional[torch.Tensor], rows: int):
+    """(total_q, H, k) of an attention's arguments, which have to fit one another."""
+    qs, ks = q_att.shape, topk_idx.shape
+    if len(qs) != 3 or qs[2] != HISA_ATT_DIM:
+        raise ValueError(f"q_att must be [total_q, H, {HISA_ATT_DIM}], got {tuple(qs)}")
+    if len(ks) != 2 or ks[0] != qs[0]:
         raise ValueError("topk_idx must be [total_q, k]")
-    if lse is not None and lse.shape != q_att.shape[:2]:
+    if lse is not None and lse.shape != qs[:2]:
         raise ValueError("lse must be [total_q, H]")
     if weights is not None and weights.numel() != rows:
         raise ValueError("weights must hold one number per cache row")
+    return qs[0], qs[1], ks[1]
 
 
 def hisa_sparse_attention_kv4(q_att: torch.Tensor, kv4: torch.Tensor, kv4_scale: torch.Tensor,
@@ -552,24 +565,31 @@ def hisa_sparse_attention_kv4(q_att: torch.Tensor, kv4: torch.Tensor, kv4_scale:
     """Attention over each query's selected tokens of the 4-bit cache; returns out bf16
     [total_q, H, 128].  weights int64 [rows], in units of HISA_WEIGHT_UNIT: the attention
     weight of every selected token, summed over the heads, is added (needs lse)."""
-    _need_kv4(kv4, kv4_scale)
-    _need_att(q_att, topk_idx, lse, weights, kv4.shape[0])
-    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32)
-    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32)
-    S = _need_lengths(cu_seqlens_q, cu_seqlens_k, None)
-    if weights is not None and lse is None:
-        raise ValueError("weights need lse")
+    dev, i32 = _device_of(q_att, "q_att"), torch.int32
+    q = _at(q_att, "q_att", torch.bfloat16, dev)
+    a = _at(kv4, "kv4", torch.uint8, dev, HISA_KV4_ROW_BYTES)
+    b = _at(kv4_scale, "kv4_scale", torch.uint8, dev, HISA_KV4_ROW_SCALES)
+    idx = _at(topk_idx, "topk_idx", i32, dev)
+    cq = _at(cu_seqlens_q, "cu_seqlens_q", i32, dev)
+    ck = _at(cu_seqlens_k, "cu_seqlens_k", i32, dev)
+    rows = kv4.shape[0]
+    if kv4_scale.shape[0] != rows:
+        raise ValueError("kv4 and kv4_scale must have the same number of rows")
+    total_q, heads, k = _att_shapes(q_att, topk_idx, lse, weights, rows)
+    S = _seqs(cu_seqlens_q, cu_seqlens_k, None)
     if out is None:
-        out = torch.empty(q_att.shape, dtype=torch.bfloat16, device=q_att.device)
-    _need(out, "out", torch.bfloat16)
-    if out.shape != q_att.shape:
+        out = torch.empty_like(q_att)
+    elif out.shape != q_att.shape:
         raise ValueError("out must have the shape of q_att")
-    _same_device(kv4, kv4_scale, q_att, topk_idx, cu_seqlens_q, cu_seqlens_k, out, lse, weights)
-    _check(lib().hisa_sparse_attention_kv4(_ptr(q_att), _ptr(kv4), _ptr(kv4_scale),
-                                           _ptr(topk_idx), _ptr(cu_seqlens_q),
-                                           _ptr(cu_seqlens_k), S, q_att.shape[0], q_att.shape[1],
-                                           topk_idx.shape[1], float(scale), _ptr(out), _ptr(lse),
-                                           _ptr(weights), _stream(stream)),
+    o = _at(out, "out", torch.bfloat16, dev)
+    ls = None if lse is None else _at(lse, "lse", torch.float32, dev)
+    w = None
+    if weights is not None:
+        if lse is None:
+            raise ValueError("weights need lse")
+        w = _at(weights, "weights", torch.int64, dev)
+    _check(lib().hisa_sparse_attention_kv4(q, a, b, idx, cq, ck, S, total_q, heads, k, scale, o,
+                                           ls, w, _raw_stream(stream, dev)),
            "hisa_sparse_attention_kv4")
     return out
 
@@ -579,18 +599,18 @@ def hisa_token_weights(q_att: torch.Tensor, k_att: torch.Tensor, topk_idx: torch
                        scale: float, weights: torch.Tensor, stream=None) -> torch.Tensor:
     """Add the attention weight of every selected token of the bf16 cache, summed over the
     heads, to weights int64 [rows] (units of HISA_WEIGHT_UNIT); returns weights."""
-    _need(k_att, "k_att", torch.bfloat16, HISA_ATT_DIM)
-    _need(lse, "lse", torch.float32)
-    _need(weights, "weights", torch.int64)
-    _need_att(q_att, topk_idx, lse, weights, k_att.shape[0])
-    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32)
-    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32)
-    S = _need_lengths(cu_seqlens_q, cu_seqlens_k, None)
-    _same_device(k_att, q_att, topk_idx, lse, cu_seqlens_q, cu_seqlens_k, weights)
-    _check(lib().hisa_token_weights(_ptr(q_att), _ptr(k_att), _ptr(topk_idx), _ptr(lse),
-                                    _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), S, q_att.shape[0],
-                                    q_att.shape[1], topk_idx.shape[1], float(scale),
-                                    _ptr(weights), _stream(stream)), "hisa_token_weights")
+    dev, i32 = _device_of(q_att, "q_att"), torch.int32
+    q = _at(q_att, "q_att", torch.bfloat16, dev)
+    ka = _at(k_att, "k_att", torch.bfloat16, dev, HISA_ATT_DIM)
+    idx = _at(topk_idx, "topk_idx", i32, dev)
+    cq = _at(cu_seqlens_q, "cu_seqlens_q", i32, dev)
+    ck = _at(cu_seqlens_k, "cu_seqlens_k", i32, dev)
+    ls = _at(lse, "lse", torch.float32, dev)
+    w = _at(weights, "weights", torch.int64, dev)
+    total_q, heads, k = _att_shapes(q_att, topk_idx, lse, weights, k_att.shape[0])
+    S = _seqs(cu_seqlens_q, cu_seqlens_k, None)
+    _check(lib().hisa_token_weights(q, ka, idx, ls, cq, ck, S, total_q, heads, k, scale, w,
+                                    _raw_stream(stream, dev)), "hisa_token_weights")
     return weights
 
 
@@ -600,25 +620,23 @@ def hisa_evict_select(weights: torch.Tensor, cu_seqlens_k: torch.Tensor,
                       kept_len: Optional[torch.Tensor] = None, stream=None):
     """Which tokens of every sequence stay: the first n_sink, the last n_recent and those of
     the largest weights, keep[s] in all; returns (kept int32 [rows], kept_len int32 [S])."""
-    _need(weights, "weights", torch.int64)
-    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32)
-    _need(seqlens_k, "seqlens_k", torch.int32, optional=True)
-    _need(keep, "keep", torch.int32)
-    S = _need_lengths(None, cu_seqlens_k, seqlens_k)
+    dev, i32 = _device_of(weights, "weights"), torch.int32
+    w = _at(weights, "weights", torch.int64, dev)
+    ck = _at(cu_seqlens_k, "cu_seqlens_k", i32, dev)
+    n = None if seqlens_k is None else _at(seqlens_k, "seqlens_k", i32, dev)
+    b = _at(keep, "keep", i32, dev)
+    S, rows = _seqs(None, cu_seqlens_k, seqlens_k), weights.numel()
     if keep.numel() != S:
         raise ValueError("keep must hold one budget per sequence")
     if kept is None:
-        kept = torch.empty(weights.numel(), dtype=torch.int32, device=weights.device)
+        kept = torch.empty(rows, dtype=i32, device=weights.device)
     if kept_len is None:
-        kept_len = torch.empty(S, dtype=torch.int32, device=weights.device)
-    _need(kept, "kept", torch.int32)
-    _need(kept_len, "kept_len", torch.int32)
-    if kept.numel() != weights.numel() or kept_len.numel() != S:
+        kept_len = torch.empty(S, dtype=i32, device=weights.device)
+    ks, kn = _at(kept, "kept", i32, dev), _at(kept_len, "kept_len", i32, dev)
+    if kept.numel() != rows or kept_len.numel() != S:
         raise ValueError("kept must hold one number per cache row, kept_len one per sequence")
-    _same_device(weights, cu_seqlens_k, seqlens_k, keep, kept, kept_len)
-    _check(lib().hisa_evict_select(_ptr(weights), _ptr(cu_seqlens_k), _ptr(seqlens_k), _ptr(keep),
-                                   S, int(max_seqlen_k), int(n_sink), int(n_recent), _ptr(kept),
-                                   _ptr(kept_len), _stream(stream)), "hisa_evict_select")
+    _check(lib().hisa_evict_select(w, ck, n, b, S, int(max_seqlen_k), int(n_sink), int(n_recent),
+                                   ks, kn, _raw_stream(stream, dev)), "hisa_evict_select")
     return kept, kept_len
 
 
@@ -627,39 +645,44 @@ class _Rows(ctypes.Structure):
                 ("row_bytes", ctypes.c_size_t)]
 
 
+_RowArray = _Rows * HISA_MAX_ROW_ARRAYS
+
+
 def hisa_evict_rows(src, dst, cu_src: torch.Tensor, cu_dst: torch.Tensor, kept: torch.Tensor,
                     kept_len: torch.Tensor, max_keep: int, stream=None) -> None:
     """Move the rows that stay (kept, kept_len of hisa_evict_select) of the row arrays src to
     the front of their regions of the arrays dst; the same tensor in both moves in place."""
     if len(src) != len(dst) or len(src) > HISA_MAX_ROW_ARRAYS:
         raise ValueError(f"src and dst must be as many arrays, at most {HISA_MAX_ROW_ARRAYS}")
-    for name, t in (("cu_src", cu_src), ("cu_dst", cu_dst), ("kept", kept),
-                    ("kept_len", kept_len)):
-        _need(t, name, torch.int32)
-    S = _need_lengths(cu_dst, cu_src, kept_len)
-    _same_device(kept, kept_len, cu_src, cu_dst, *src, *dst)
-    rows = (_Rows * max(1, len(src)))()
-    spans = []
+    dev, i32 = _device_of(kept, "kept"), torch.int32
+    ks, kn = _at(kept, "kept", i32, dev), _at(kept_len, "kept_len", i32, dev)
+    cs, cd = _at(cu_src, "cu_src", i32, dev), _at(cu_dst, "cu_dst", i32, dev)
+    S, n_rows = _seqs(cu_dst, cu_src, kept_len), kept.numel()
+    rows = _RowArray()
+    spans = []  # first and last byte behind, destinations and sources; in place counts once
     for i, (a, b) in enumerate(zip(src, dst)):
-        if a.dtype != b.dtype or a.dim() < 1 or a.shape[1:] != b.shape[1:]:
+        dt = a.dtype
+        pa, pb = _at(a, "a source", dt, dev), _at(b, "a destination", b.dtype, dev)
+        sa, sb = a.shape, b.shape
+        if dt is not b.dtype or not sa or len(sa) != len(sb) or sa[1:] != sb[1:]:
             raise ValueError("a source and its destination must have rows of one type and shape")
-        if not a.is_contiguous() or not b.is_contiguous():
-            raise ValueError("row arrays must be contiguous")
-        if a.shape[0] != kept.numel():
+        if sa[0] != n_rows:
             raise ValueError("kept must hold one number per source row")
-        pa, pb = a.data_ptr(), b.data_ptr()
-        row = a.element_size()
-        for n in a.shape[1:]:
-            row *= n
-        rows[i] = _Rows(pa, pb, row)
-        in_place = pa == pb and a.shape == b.shape
-        spans.append((pa, pa + row * a.shape[0], pb, pb + row * b.shape[0], in_place))
-    for i, x in enumerate(spans):
-        for j, y in enumerate(spans):
-            if x[2] < y[1] and y[0] < x[3] and not (i == j and x[4]):
-                raise ValueError("a destination overlaps a source")
-            if i != j and x[2] < y[3] and y[2] < x[3]:
-                raise ValueError("two destinations overlap")
-    _check(lib().hisa_evict_rows(rows, len(src), _ptr(cu_src), _ptr(cu_dst), _ptr(kept),
-                                 _ptr(kept_len), S, int(max_keep), _stream(stream)),
-           "hisa_evict_rows")
+        nbytes = a.nbytes
+        row = nbytes // n_rows if n_rows else 4
+        r = rows[i]
+        r.src, r.dst, r.row_bytes = pa, pb, row
+        spans.append((pb, pb + b.nbytes, 1))
+        if pa != pb or sa != sb:
+            spans.append((pa, pa + nbytes, 0))
+    # in order of their starts, a span may touch none before it, unless both are sources
+    spans.sort()
+    end = end_dst = 0
+    for a, b, is_dst in spans:
+        if a < (end if is_dst else end_dst) and a < b:
+            raise ValueError("a destination overlaps a source, or two destinations overlap")
+        end = max(end, b)
+        if is_dst:
+            end_dst = max(end_dst, b)
+    _check(lib().hisa_evict_rows(rows, len(src), cs, cd, ks, kn, S, int(max_keep),
+                                 _raw_stream(stream, dev)), "hisa_evict_rows")

@@ -63,16 +63,12 @@ cudaError_t launch_kv4_load(const uint8_t *kv4, const uint8_t *kv4_scale, const 
 cudaError_t launch_attention_kv4(const uint16_t *q, const uint8_t *kv4, const uint8_t *kv4_scale,
                                  const int32_t *idx, const int32_t *cu_q, const int32_t *cu_k,
                                  int S, int total_q, int H, int topk, float scale, uint16_t *out,
-                                 float *lse, int num_sms, int *status, cudaStream_t st);
+                                 float *lse, int64_t *weights, int num_sms, int *status,
+                                 cudaStream_t st);
 cudaError_t launch_token_weights(const uint16_t *q, const uint16_t *k, const int32_t *idx,
                                  const float *lse, const int32_t *cu_q, const int32_t *cu_k, int S,
                                  int total_q, int H, int topk, float scale, int64_t *weights,
                                  int num_sms, int *status, cudaStream_t st);
-cudaError_t launch_token_weights_kv4(const uint16_t *q, const uint8_t *kv4,
-                                     const uint8_t *kv4_scale, const int32_t *idx,
-                                     const float *lse, const int32_t *cu_q, const int32_t *cu_k,
-                                     int S, int total_q, int H, int topk, float scale,
-                                     int64_t *weights, int num_sms, int *status, cudaStream_t st);
 cudaError_t launch_evict_select(const int64_t *weights, const int32_t *cu_k,
                                 const int32_t *seqlens, const int32_t *keep, int S,
                                 int max_seqlen_k, int n_sink, int n_recent, int32_t *kept,
@@ -574,14 +570,10 @@ hisa_status hisa_sparse_attention_kv4(const hisa_bf16 *q_att, const uint8_t *kv4
     return HISA_ERR_UNALIGNED;
   int *st = status_word();
   if (!st) return HISA_ERR_CUDA;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_attention_kv4(q_att, kv4, kv4_scale, topk_idx, cu_seqlens_q, cu_seqlens_k,
-                                       num_seqs, total_q, num_heads, k, scale, out, lse, num_sms(),
-                                       st, s);
-  if (e == cudaSuccess && weights)
-    e = launch_token_weights_kv4(q_att, kv4, kv4_scale, topk_idx, lse, cu_seqlens_q, cu_seqlens_k,
-                                 num_seqs, total_q, num_heads, k, scale, weights, num_sms(), st, s);
-  return from_cuda(e);
+  return from_cuda(launch_attention_kv4(q_att, kv4, kv4_scale, topk_idx, cu_seqlens_q,
+                                        cu_seqlens_k, num_seqs, total_q, num_heads, k, scale, out,
+                                        lse, weights, num_sms(), st,
+                                        static_cast<cudaStream_t>(stream)));
 }
 
 hisa_status hisa_token_weights(const hisa_bf16 *q_att, const hisa_bf16 *k_att,

@@ -42,11 +42,15 @@ constexpr int A4_STEP = 32;                                   // tokens of a war
 constexpr int A4_CODES = A4_STEP * KV4_ROW;                   // 4096 bytes
 constexpr int A4_STAGE = A4_CODES + A4_STEP * KV4_NS;         // 4608
 constexpr int A4_MAX_CLUSTER = 8;
+constexpr int A4_SCORE_TOKENS = 512;  // tokens of a CTA that keeps its scores for the weights
 constexpr float A4_TAU = 8.f;    // tolerated growth of a head's maximum, in powers of two
 constexpr int A4_OSTRIDE = KV4_DIM + 4;                       // padded row of partial outputs
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float LOG2E = 1.4426950408889634f, LOG2E_LO = 1.92596303e-8f, LN2 = 0.6931471805599453f;
 
+constexpr int A4_WARPS = 4, A4_THREADS = A4_WARPS * 32;
 __host__ __device__ constexpr int a4_stages(int MT) { return MT == 1 ? 3 : 4; }
+// CTAs of an SM: one or two 16-head tiles in up to 168 or 255 registers per thread
+__host__ __device__ constexpr int a4_ctas(int MT) { return MT == 1 ? 3 : 2; }
 // a warp's ring, which later holds its partial output
 __host__ __device__ constexpr int a4_ring(int MT) { return a4_stages(MT) * A4_STAGE; }
 static_assert(16 * A4_OSTRIDE * 4 <= a4_ring(1) && 32 * A4_OSTRIDE * 4 <= a4_ring(2),
@@ -64,6 +68,14 @@ __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *sr
                "r"(ok ? 16 : 0)
                : "memory");
 }
+// p + j * KV4_ROW in one multiply-add
+__device__ __forceinline__ const uint8_t *row_of(const uint8_t *p, int j) {
+  uint64_t r;
+  asm("mad.wide.u32 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "r"(j), "r"(KV4_ROW), "l"(reinterpret_cast<uint64_t>(p)));
+  return reinterpret_cast<const uint8_t *>(r);
+}
 template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -80,525 +92,253 @@ __device__ __forceinline__ void q_shift(uint32_t max_bits, float &up, float &dow
   down = __uint_as_float((uint32_t)(127 - sh) << 23);
 }
 
-// Query fragments of heads 16 mt + g and + g + 8: fragment ks = 2 w + half holds the
-// dimension pairs (d, d + 4) of word w (32c + 8w ..), d = 0 and 1 (half 0) or 2 and 3.
-// `down` of the two heads comes back in dn.  Heads >= H are zeros.
-__device__ __forceinline__ void load_q_frags(const uint16_t *__restrict__ q, size_t row, int H, int mt,
-                                             int lane, uint32_t (&f)[8][4], float (&dn)[2]) {
+// The query fragments, in shared memory as [mt][ks][lane] of 16 bytes: fragment ks = 2w +
+// half of a 16-head tile holds the dimension pairs (d, d + 4) of word w (32c + 8w ..), d = 0
+// and 1 (half 0) or 2 and 3; heads >= H are zeros.  In registers (32 for 16 heads) they
+// left the compiler too few to overlap its work: 663 us instead of 637 for 8192 queries of
+// 16 heads on 2048 tokens each.
+// Each of the W warps that share a query looks at all of it, since it needs the heads' powers
+// of two (f: what takes its raw scores, of heads g and g + 8, to exponents of two), and
+// converts its part; the caller synchronises them.
+template <int MT, int W>
+__device__ __forceinline__ void load_query(const uint16_t *__restrict__ q, size_t row, int H,
+                                           float scale, uint4 *qs, int lane, int warp,
+                                           float (&f)[MT][2]) {
   const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-  for (int r = 0; r < 2; r++) {
-    const int h = 16 * mt + g + 8 * r;
-    uint4 w[4];
-    uint32_t mx = 0;
+  for (int mt = 0; mt < MT; mt++) {
+    uint4 w[2][4];
+    float up[2];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      w[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < H)
-        w[i] = __ldg(reinterpret_cast<const uint4 *>(q + (row * H + h) * KV4_DIM + 32 * c) + i);
-      mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu),
-                                 __vmaxu2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu)));
+    for (int r = 0; r < 2; r++) {
+      const int h = 16 * mt + g + 8 * r;
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        w[r][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (h < H)
+          w[r][i] =
+              __ldg(reinterpret_cast<const uint4 *>(q + (row * H + h) * KV4_DIM + 32 * c) + i);
+        const uint4 v = w[r][i];
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                   __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+      }
+      mx = max(mx & 0xFFFFu, mx >> 16);
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      float down;
+      q_shift(mx, up[r], down);
+      f[mt][r] = down * (scale * LOG2E);
     }
-    mx = max(mx & 0xFFFFu, mx >> 16);
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    float up;
-    q_shift(mx, up, dn[r]);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      // dimensions 0..7 of the word: pairs (0,4) (1,5) (2,6) (3,7)
-      const float x[8] = {bf_lo(w[i].x), bf_hi(w[i].x), bf_lo(w[i].y), bf_hi(w[i].y),
-                          bf_lo(w[i].z), bf_hi(w[i].z), bf_lo(w[i].w), bf_hi(w[i].w)};
+    for (int i = 0; i < 4; i++)
+      if ((4 * mt + i) % W == warp % W) {
+        uint32_t t[2][4];  // [r][pair]
 #pragma unroll
-      for (int p = 0; p < 4; p++)
-        f[2 * i + (p >> 1)][2 * (p & 1) + r] =
-            as_u32(__floats2half2_rn(x[p] * up, x[p + 4] * up));
+        for (int r = 0; r < 2; r++) {
+          const uint4 v = w[r][i];
+          // dimensions 0..7 of the word: pairs (0,4) (1,5) (2,6) (3,7)
+          t[r][0] = as_u32(__floats2half2_rn(bf_lo(v.x) * up[r], bf_lo(v.z) * up[r]));
+          t[r][1] = as_u32(__floats2half2_rn(bf_hi(v.x) * up[r], bf_hi(v.z) * up[r]));
+          t[r][2] = as_u32(__floats2half2_rn(bf_lo(v.y) * up[r], bf_lo(v.w) * up[r]));
+          t[r][3] = as_u32(__floats2half2_rn(bf_hi(v.y) * up[r], bf_hi(v.w) * up[r]));
+        }
+        uint4 *d = qs + (mt * 8 + 2 * i) * 32 + lane;
+        d[0] = make_uint4(t[0][0], t[1][0], t[0][1], t[1][1]);
+        d[32] = make_uint4(t[0][2], t[1][2], t[0][3], t[1][3]);
+      }
+  }
+}
+
+// A lane's places in a ring stage: the swizzle of a token's row depends on the token modulo
+// 8 only, so every other token is a constant distance away.
+struct LanePlaces {
+  uint32_t kc, ks;        // token g: the lane's 16 key bytes, its two key scales
+  uint32_t v0, v1;        // tokens 2c and 2c + 1: the lane's 8 value bytes
+  uint32_t s0, s1;        // and their value scales
+  uint32_t d0, d1;        // copies: chunks lane % 4 and lane % 4 + 4 of token lane / 4
+  __device__ __forceinline__ explicit LanePlaces(int lane) {
+    const int g = lane >> 2, c = lane & 3, t = 2 * c;
+    kc = g * KV4_ROW + (a4_chunk(g, c) << 4);
+    ks = A4_CODES + g * KV4_NS + 2 * c;
+    v0 = t * KV4_ROW + (a4_chunk(t, 4 + (g >> 1)) << 4) + (g & 1) * 8;
+    v1 = (t + 1) * KV4_ROW + (a4_chunk(t + 1, 4 + (g >> 1)) << 4) + (g & 1) * 8;
+    s0 = A4_CODES + t * KV4_NS + 8 + g;
+    s1 = s0 + KV4_NS;
+    d0 = g * KV4_ROW + (a4_chunk(g, c) << 4);
+    d1 = g * KV4_ROW + (a4_chunk(g, c + 4) << 4);
+  }
+};
+
+// Raw scores of the tokens 8j .. 8j + 7 of a ring stage: s[mt] is their score fragment.
+// qs: the query fragments at this lane's place.
+template <int MT>
+__device__ __forceinline__ void kv4_scores(const uint8_t *stage, int j, const LanePlaces &lp,
+                                           const uint4 *qs, uint32_t magic,
+                                           float (&s)[MT][4][4]) {
+  const uint4 kw = *reinterpret_cast<const uint4 *>(stage + lp.kc + j * 8 * KV4_ROW);
+  const uint32_t sb = *reinterpret_cast<const uint16_t *>(stage + lp.ks + j * 8 * KV4_NS);
+  const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    // both halves of the scale pair: byte 0 (words 0, 1) or byte 1 (words 2, 3)
+    const __half2 sc = as_half2(__byte_perm(sb, 0u, i < 2 ? 0x4040 : 0x4141) << 7);
+    const __half2 c72 = kv4_c72(sc);
+    const uint32_t b0 = kv4_pair(w[i] << 4, magic, sc, c72), b1 = kv4_pair(w[i], magic, sc, c72);
+    const uint32_t b2 = kv4_pair(w[i] >> 4, magic, sc, c72);
+    const uint32_t b3 = kv4_pair(w[i] >> 8, magic, sc, c72);
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++) {
+      const uint4 qa = qs[(mt * 8 + 2 * i) * 32], qb = qs[(mt * 8 + 2 * i + 1) * 32];
+      if (i == 0)
+        mma_f16_first(s[mt][j], qa.x, qa.y, qa.z, qa.w, b0, b1);
+      else
+        mma_f16(s[mt][j], qa.x, qa.y, qa.z, qa.w, b0, b1);
+      mma_f16(s[mt][j], qb.x, qb.y, qb.z, qb.w, b2, b3);
     }
   }
 }
 
-// Query fragments of one 16-head tile: in registers for one tile, in shared memory (a
-// lane's 16 bytes per fragment) for two, whose outputs leave no room for them.
-template <int MT>
-struct QFrags;
-template <>
-struct QFrags<1> {
-  uint32_t f[8][4];
-  __device__ __forceinline__ uint4 get(int, int ks) const {
-    return make_uint4(f[ks][0], f[ks][1], f[ks][2], f[ks][3]);
-  }
-};
-template <>
-struct QFrags<2> {
-  const uint4 *s;  // [mt][ks][lane]
-  int lane;
-  __device__ __forceinline__ uint4 get(int mt, int ks) const {
-    return s[(mt * 8 + ks) * 32 + lane];
+// The value fragments' raw material of 16 tokens (half i of a stage).
+struct ValueRaw {
+  uint2 v[4];              // nibbles of the tokens 2c, 2c + 1, 2c + 8, 2c + 9
+  __half2 s0, s1, k0, k1;  // their scales in pairs, and -72 times them
+  __device__ __forceinline__ void load(const uint8_t *stage, int i, const LanePlaces &lp) {
+    uint32_t sb[4];
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      const int t = 16 * i + 8 * (u >> 1);
+      v[u] = *reinterpret_cast<const uint2 *>(stage + ((u & 1) ? lp.v1 : lp.v0) + t * KV4_ROW);
+      sb[u] = stage[((u & 1) ? lp.s1 : lp.s0) + t * KV4_NS];
+    }
+    s0 = as_half2(__byte_perm(sb[0], sb[1], 0x5410) << 7);
+    s1 = as_half2(__byte_perm(sb[2], sb[3], 0x5410) << 7);
+    k0 = kv4_c72(s0);
+    k1 = kv4_c72(s1);
   }
 };
 
-// Raw scores of the 32 tokens in a ring stage: s[mt][j][.] is the score fragment of the
-// 8 tokens 8j .. 8j + 7.
+// o += weights p (of 16 tokens: half i) times dimensions 8b .. 8b + 7 of every group
 template <int MT>
-__device__ __forceinline__ void kv4_scores(const uint8_t *stage, const QFrags<MT> &qf, int lane,
-                                           float (&s)[MT][4][4]) {
-  const int g = lane >> 2, c = lane & 3;
+__device__ __forceinline__ void kv4_values(const ValueRaw &r, int i, int b,
+                                           const uint32_t (&p)[MT][4][2], uint32_t magic,
+                                           float (&o)[MT][16][4]) {
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
-    const int t = 8 * j + g;
-    const uint4 kw =
-        *reinterpret_cast<const uint4 *>(stage + t * KV4_ROW + (a4_chunk(t, c) << 4));
-    const uint32_t sb =
-        *reinterpret_cast<const uint16_t *>(stage + A4_CODES + t * KV4_NS + 2 * c);
-    const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+  for (int w = 2 * b; w < 2 * b + 2; w++) {  // dimensions 4w .. 4w + 3
+    const uint32_t sel = (w & 1) ? 0x7632 : 0x5410;
+    const uint32_t r0 =
+        b ? __byte_perm(r.v[0].y, r.v[1].y, sel) : __byte_perm(r.v[0].x, r.v[1].x, sel);
+    const uint32_t r1 =
+        b ? __byte_perm(r.v[2].y, r.v[3].y, sel) : __byte_perm(r.v[2].x, r.v[3].x, sel);
 #pragma unroll
-    for (int mt = 0; mt < MT; mt++)
+    for (int d = 0; d < 4; d++) {
+      const uint32_t b0 = kv4_pair(d == 0 ? r0 << 4 : r0 >> (4 * d - 4), magic, r.s0, r.k0);
+      const uint32_t b1 = kv4_pair(d == 0 ? r1 << 4 : r1 >> (4 * d - 4), magic, r.s1, r.k1);
 #pragma unroll
-      for (int e = 0; e < 4; e++) s[mt][j][e] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      // both halves of the scale pair: byte 0 (words 0, 1) or byte 1 (words 2, 3)
-      const __half2 sc = as_half2(__byte_perm(sb, 0u, i < 2 ? 0x4040 : 0x4141) << 7);
-      const __half2 c72 = kv4_c72(sc);
-      const uint32_t b0 = kv4_pair(w[i] << 4, sc, c72), b1 = kv4_pair(w[i], sc, c72);
-      const uint32_t b2 = kv4_pair(w[i] >> 4, sc, c72), b3 = kv4_pair(w[i] >> 8, sc, c72);
-#pragma unroll
-      for (int mt = 0; mt < MT; mt++) {
-        const uint4 qa = qf.get(mt, 2 * i), qb = qf.get(mt, 2 * i + 1);
-        mma_f16(s[mt][j], qa.x, qa.y, qa.z, qa.w, b0, b1);
-        mma_f16(s[mt][j], qb.x, qb.y, qb.z, qb.w, b2, b3);
-      }
+      for (int mt = 0; mt < MT; mt++)
+        mma_f16(o[mt][4 * w + d], p[mt][2 * i][0], p[mt][2 * i][1], p[mt][2 * i + 1][0],
+                p[mt][2 * i + 1][1], b0, b1);
     }
   }
 }
 
 // A warp's walk over its steps: the token ids are read one step ahead of the copies, the
-// copies run NST - 1 steps ahead of the products.
-template <int NST>
+// copies run AHEAD steps ahead of the products, over NST stages: the NST - 1 - AHEAD steps
+// before the current one stay readable.
+// VALUES: the value halves of the rows are copied too.
+template <int NST, int AHEAD, bool VALUES>
 struct Ring {
   const int32_t *irow;
-  int e0, e1, nsteps, stride, first;  // entries [e0, e1); steps first, first + stride, ...
+  int e1, nsteps, next_e, stride;   // this lane's entry of the next step to read, up to e1
+  int first_e;                      // and of the first
   int kcap;
-  size_t kbase;
-  const uint8_t *kv4, *kv4_scale;
+  const uint8_t *codes, *scales;    // the region's first row; codes at this lane's chunk
   uint8_t *ring;
-  int lane;
-  int next_tok;             // this lane's token of the next step to copy (-1 = none)
-  uint32_t mask[NST];       // valid tokens of the steps in flight, oldest first
+  uint32_t slot, fill;              // bytes to the stage of the next step, and of the next copy
+  int next_tok;                     // this lane's token of the next step to copy (-1 = none)
+  uint32_t mask[AHEAD];             // valid tokens of the steps in flight, oldest first
   bool bad;
 
-  __device__ __forceinline__ int token(int n) const {
-    const int e = e0 + (first + n * stride) * A4_STEP + lane;
-    return (n < nsteps && e < e1) ? __ldg(irow + e) : -1;
+  // steps first, first + stride, ... of the entries [e0, e1)
+  __device__ __forceinline__ void init(const int32_t *row, int e0, int end, int first, int step,
+                                       int kbase, int cap, const uint8_t *kv4,
+                                       const uint8_t *kv4_scale, uint8_t *mem, int lane) {
+    irow = row;
+    e1 = end;
+    const int steps = end > e0 ? (end - e0 + A4_STEP - 1) / A4_STEP : 0;
+    nsteps = steps > first ? (steps - first + step - 1) / step : 0;
+    first_e = next_e = e0 + first * A4_STEP + lane;
+    stride = step * A4_STEP;
+    kcap = cap;
+    codes = kv4 + (size_t)kbase * KV4_ROW + (lane & 3) * 16;
+    scales = kv4_scale + (size_t)kbase * KV4_NS;
+    ring = mem;
+    slot = fill = 0;
+    bad = false;
+    read();
   }
-  // start the copy of step n into stage n % NST
-  __device__ __forceinline__ uint32_t copy(int n) {
+  __device__ __forceinline__ void read() {
+    next_tok = next_e < e1 ? __ldg(irow + next_e) : -1;
+    next_e += stride;
+  }
+  static __device__ __forceinline__ uint32_t after(uint32_t at) {
+    return at == (NST - 1) * A4_STAGE ? 0 : at + A4_STAGE;
+  }
+  // start the copy of the next step; the valid tokens in it
+  __device__ __forceinline__ uint32_t copy(const LanePlaces &lp, int lane) {
     int j = next_tok;
-    next_tok = token(n + 1);
+    read();
     if (j >= kcap) {
       bad = true;
       j = -1;
     }
     const uint32_t valid = __ballot_sync(0xffffffffu, j >= 0);
-    if (n < nsteps && valid) {
-      const uint32_t dst = smem_u32(ring + (n % NST) * A4_STAGE);
-      const int chunk = lane & 7;
+    const uint32_t dst = smem_u32(ring) + fill;
+    fill = after(fill);
+    const uint32_t a0 = dst + lp.d0, a1 = dst + lp.d1;
+    // four lanes copy 64 bytes of a token together, eight tokens at a time
+    if (valid == 0xffffffffu) {
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        const int t = 4 * i + (lane >> 3);
-        const int jt = __shfl_sync(0xffffffffu, j, t);
-        cp_async_16_or_zero(dst + t * KV4_ROW + (a4_chunk(t, chunk) << 4),
-                            kv4 + (kbase + (size_t)max(jt, 0)) * KV4_ROW + chunk * 16, jt >= 0);
+      for (int i = 0; i < 4; i++) {
+        const uint8_t *src = row_of(codes, __shfl_sync(0xffffffffu, j, 8 * i + (lane >> 2)));
+        cp_async_16(a0 + i * 8 * KV4_ROW, src);
+        if (VALUES) cp_async_16(a1 + i * 8 * KV4_ROW, src + 64);
+      }
+      cp_async_16(dst + A4_CODES + lane * KV4_NS, scales + (size_t)(uint32_t)j * KV4_NS);
+    } else if (valid) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int jt = __shfl_sync(0xffffffffu, j, 8 * i + (lane >> 2));
+        const uint8_t *src = row_of(codes, max(jt, 0));
+        cp_async_16_or_zero(a0 + i * 8 * KV4_ROW, src, jt >= 0);
+        if (VALUES) cp_async_16_or_zero(a1 + i * 8 * KV4_ROW, src + 64, jt >= 0);
       }
       cp_async_16_or_zero(dst + A4_CODES + lane * KV4_NS,
-                          kv4_scale + (kbase + (size_t)max(j, 0)) * KV4_NS, j >= 0);
+                          scales + (size_t)(uint32_t)max(j, 0) * KV4_NS, j >= 0);
     }
     cp_async_commit();
     return valid;
   }
-  __device__ __forceinline__ void start() {
-    bad = false;
-    next_tok = token(0);
+  __device__ __forceinline__ void start(const LanePlaces &lp, int lane) {
 #pragma unroll
-    for (int n = 0; n < NST - 1; n++) mask[n] = copy(n);
+    for (int n = 0; n < AHEAD; n++) mask[n] = copy(lp, lane);
   }
-  // wait for step n; its stage and the mask of its valid tokens
-  __device__ __forceinline__ const uint8_t *arrive(int n, uint32_t &valid) {
-    cp_async_wait_group<NST - 2>();
-    __syncwarp();  // the step has landed for every lane, and stage (n - 1) % NST is read
+  // start one more copy, wait for the next step; its stage and the mask of its valid tokens
+  __device__ __forceinline__ const uint8_t *arrive(const LanePlaces &lp, int lane,
+                                                   uint32_t &valid) {
+    __syncwarp();  // every lane has read the stage that is filled now
+    const uint32_t more = copy(lp, lane);
     valid = mask[0];
 #pragma unroll
-    for (int i = 0; i + 2 < NST; i++) mask[i] = mask[i + 1];
-    mask[NST - 2] = copy(n + NST - 1);
-    return ring + (n % NST) * A4_STAGE;
+    for (int i = 0; i + 1 < AHEAD; i++) mask[i] = mask[i + 1];
+    mask[AHEAD - 1] = more;
+    cp_async_wait_group<AHEAD>();
+    __syncwarp();  // the step has landed for every lane
+    const uint8_t *stage = ring + slot;
+    slot = after(slot);
+    return stage;
   }
 };
-
-template <int MT>
-struct A4Smem {
-  static constexpr int QBYTES = MT == 1 ? 0 : MT * 8 * 32 * 16;
-  // ring of every warp | query fragments | m, l of every warp and head | merge weights
-  __host__ __device__ static constexpr size_t bytes(int warps) {
-    return (size_t)warps * a4_ring(MT) + QBYTES + (size_t)warps * 16 * MT * 8 +
-           (size_t)16 * MT * 8 + (size_t)16 * MT * A4_MAX_CLUSTER * 8;
-  }
-};
-
-template <int MT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, MT == 1 ? 12 / WARPS : 8 / WARPS)
-attn_kv4_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict__ kv4,
-                const uint8_t *__restrict__ kv4_scale, const int32_t *__restrict__ idx,
-                const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, int S, int H,
-                int topk, int per_cta, float scale, uint16_t *__restrict__ out,
-                float *__restrict__ lse, int *status) {
-  extern __shared__ __align__(16) uint8_t a4_smem[];
-  constexpr int NST = a4_stages(MT), RING = a4_ring(MT), NH = 16 * MT;
-  cg::cluster_group cl = cg::this_cluster();
-  const int C = (int)cl.num_blocks(), me = (int)cl.block_rank();
-  const int row = blockIdx.x / C;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, c = lane & 3;
-  const float NEG = -__int_as_float(0x7f800000);
-  uint8_t *qs = a4_smem + WARPS * RING;
-  float *wm = reinterpret_cast<float *>(qs + A4Smem<MT>::QBYTES);  // [WARPS][NH]
-  float *wl = wm + WARPS * NH;                                     // [WARPS][NH]
-  float *cm = wl + WARPS * NH, *cs = cm + NH;  // the CTA's maximum and sum per head
-  float *xm = cs + NH, *xl = xm + NH * A4_MAX_CLUSTER;  // the cluster's, per own head and CTA
-
-  const int s = find_seq(cu_q, S, row);
-  const int kbase = __ldg(cu_k + s);
-  Ring<NST> ring;
-  ring.e0 = me * per_cta;
-  ring.e1 = min(topk, ring.e0 + per_cta);
-  const int steps = ring.e1 > ring.e0 ? (ring.e1 - ring.e0 + A4_STEP - 1) / A4_STEP : 0;
-  ring.irow = idx + (size_t)row * topk;
-  ring.first = warp;
-  ring.stride = WARPS;
-  ring.nsteps = steps > warp ? (steps - warp + WARPS - 1) / WARPS : 0;
-  ring.kcap = __ldg(cu_k + s + 1) - kbase;
-  ring.kbase = (size_t)kbase;
-  ring.kv4 = kv4;
-  ring.kv4_scale = kv4_scale;
-  ring.ring = a4_smem + warp * RING;
-  ring.lane = lane;
-  ring.start();
-
-  QFrags<MT> qf;
-  float f[MT][2];  // score -> power-of-two exponent, of heads g and g + 8
-  if constexpr (MT == 1) {
-    load_q_frags(q, (size_t)row, H, 0, lane, qf.f, f[0]);
-  } else {
-    uint4 *sq = reinterpret_cast<uint4 *>(qs);
-    qf.s = sq;
-    qf.lane = lane;
-#pragma unroll
-    for (int mt = 0; mt < MT; mt++) {
-      uint32_t t[8][4];
-      load_q_frags(q, (size_t)row, H, mt, lane, t, f[mt]);
-      // every warp computes every fragment (it needs the shifts) and stores its part
-#pragma unroll
-      for (int ks = 0; ks < 8; ks++)
-        if ((mt * 8 + ks) % WARPS == warp)
-          sq[(mt * 8 + ks) * 32 + lane] = make_uint4(t[ks][0], t[ks][1], t[ks][2], t[ks][3]);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-    for (int r = 0; r < 2; r++) f[mt][r] *= scale * LOG2E;
-
-  float o[MT][16][4];
-  float m[MT][2], l[MT][2];
-#pragma unroll
-  for (int mt = 0; mt < MT; mt++) {
-#pragma unroll
-    for (int t = 0; t < 16; t++)
-#pragma unroll
-      for (int e = 0; e < 4; e++) o[mt][t][e] = 0.f;
-#pragma unroll
-    for (int r = 0; r < 2; r++) {
-      m[mt][r] = NEG;
-      l[mt][r] = 0.f;
-    }
-  }
-
-  for (int n = 0; n < ring.nsteps; n++) {
-    uint32_t valid;
-    const uint8_t *stage = ring.arrive(n, valid);
-    if (!valid) continue;
-    float x[MT][4][4];
-    kv4_scores<MT>(stage, qf, lane, x);
-    bool over = false;
-#pragma unroll
-    for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-      for (int j = 0; j < 4; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const bool live = (valid >> (8 * j + 2 * c + (e & 1))) & 1u;
-          x[mt][j][e] = live ? x[mt][j][e] * f[mt][e >> 1] : NEG;
-          over |= x[mt][j][e] > m[mt][e >> 1] + A4_TAU;
-        }
-    // the reference maxima rise (and sums and outputs are rescaled) only where a score
-    // exceeds one by 2^TAU; a first score always does
-    if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-      for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-        for (int r = 0; r < 2; r++) {
-          float mx = m[mt][r];
-#pragma unroll
-          for (int j = 0; j < 4; j++)
-            mx = fmaxf(mx, fmaxf(x[mt][j][2 * r], x[mt][j][2 * r + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float a = mx == NEG ? 1.f : ex2(m[mt][r] - mx);
-          m[mt][r] = mx;
-          l[mt][r] *= a;
-#pragma unroll
-          for (int t = 0; t < 16; t++) {
-            o[mt][t][2 * r] *= a;
-            o[mt][t][2 * r + 1] *= a;
-          }
-        }
-    }
-    uint32_t p[MT][4][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-      for (int r = 0; r < 2; r++) {
-        const float mu = m[mt][r] == NEG ? 0.f : m[mt][r];
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          const float p0 = ex2(x[mt][j][2 * r] - mu), p1 = ex2(x[mt][j][2 * r + 1] - mu);
-          l[mt][r] += p0 + p1;
-          p[mt][j][r] = as_u32(__floats2half2_rn(p0, p1));
-        }
-      }
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-      uint2 v[4];       // nibbles of tokens 2c, 2c + 1, 2c + 8, 2c + 9 of this half
-      uint32_t sb[4];
-#pragma unroll
-      for (int u = 0; u < 4; u++) {
-        const int t = 16 * i + 8 * (u >> 1) + 2 * c + (u & 1);
-        v[u] = *reinterpret_cast<const uint2 *>(stage + t * KV4_ROW +
-                                                (a4_chunk(t, 4 + (g >> 1)) << 4) + (g & 1) * 8);
-        sb[u] = stage[A4_CODES + t * KV4_NS + 8 + g];
-      }
-      const __half2 s0 = as_half2((sb[0] | (sb[1] << 16)) << 7);
-      const __half2 s1 = as_half2((sb[2] | (sb[3] << 16)) << 7);
-      const __half2 k0 = kv4_c72(s0), k1 = kv4_c72(s1);
-#pragma unroll
-      for (int w = 0; w < 4; w++) {  // dimensions 4w .. 4w + 3 of the group
-        const uint32_t sel = (w & 1) ? 0x7632 : 0x5410;
-        const uint32_t r0 = __byte_perm(w < 2 ? v[0].x : v[0].y, w < 2 ? v[1].x : v[1].y, sel);
-        const uint32_t r1 = __byte_perm(w < 2 ? v[2].x : v[2].y, w < 2 ? v[3].x : v[3].y, sel);
-#pragma unroll
-        for (int d = 0; d < 4; d++) {
-          const uint32_t b0 = kv4_pair(d == 0 ? r0 << 4 : r0 >> (4 * d - 4), s0, k0);
-          const uint32_t b1 = kv4_pair(d == 0 ? r1 << 4 : r1 >> (4 * d - 4), s1, k1);
-#pragma unroll
-          for (int mt = 0; mt < MT; mt++)
-            mma_f16(o[mt][4 * w + d], p[mt][2 * i][0], p[mt][2 * i][1], p[mt][2 * i + 1][0],
-                    p[mt][2 * i + 1][1], b0, b1);
-        }
-      }
-    }
-  }
-  cp_async_wait_all();
-  __syncwarp();  // the ring is free: it takes the warp's partial output
-  if (__any_sync(0xffffffffu, ring.bad) && lane == 0) raise_status(status, HISA_ERR_INVALID_ARG);
-
-  // Partial outputs, [head][dimension] with the 4-value pieces of a 32-dimension block
-  // turned by the block so that the lanes' stores spread over the banks.
-  float *po = reinterpret_cast<float *>(ring.ring);
-#pragma unroll
-  for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-    for (int r = 0; r < 2; r++) {
-      float sum = l[mt][r];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const int h = 16 * mt + g + 8 * r;
-      if (c == 0) {
-        wm[warp * NH + h] = m[mt][r];
-        wl[warp * NH + h] = sum;
-      }
-#pragma unroll
-      for (int u = 0; u < 8; u++) {
-        // piece u of dimensions 32c ..: tiles 4 (u & 3) .., column 2c + (u >> 2)
-        const int e = 2 * r + (u >> 2), t = 4 * (u & 3);
-        *reinterpret_cast<float4 *>(po + h * A4_OSTRIDE + 32 * c + 4 * (u ^ (2 * c))) =
-            make_float4(o[mt][t][e], o[mt][t + 1][e], o[mt][t + 2][e], o[mt][t + 3][e]);
-      }
-    }
-  __syncthreads();
-  // factors of the CTA's warps: 2^(m_w - m); a share with no score has the factor 0
-  if (tid < NH) {
-    float mx = NEG, sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < WARPS; w++) mx = fmaxf(mx, wm[w * NH + tid]);
-#pragma unroll
-    for (int w = 0; w < WARPS; w++) {
-      const float mw = wm[w * NH + tid];
-      const float a = mw == NEG ? 0.f : ex2(mw - mx);
-      // a share that holds a NaN keeps it whatever its maximum says
-      const float lw = wl[w * NH + tid];
-      wm[w * NH + tid] = lw != lw ? lw : a;
-      sum += lw != lw ? lw : a * lw;
-    }
-    cm[tid] = mx;
-    cs[tid] = sum;
-  }
-  __syncthreads();
-  if (C == 1) {
-    for (int x = tid; x < H * (KV4_DIM / 4); x += WARPS * 32) {
-      const int h = x >> 5, b = (x >> 3) & 3, u = x & 7;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < WARPS; w++) {
-        const float a = wm[w * NH + h];
-        const float4 v = *reinterpret_cast<const float4 *>(
-            reinterpret_cast<const float *>(a4_smem + w * RING) + h * A4_OSTRIDE + 32 * b +
-            4 * (u ^ (2 * b)));
-        acc.x = fmaf(a, v.x, acc.x);
-        acc.y = fmaf(a, v.y, acc.y);
-        acc.z = fmaf(a, v.z, acc.z);
-        acc.w = fmaf(a, v.w, acc.w);
-      }
-      const float L = cs[h], inv = L == 0.f ? 0.f : 1.f / L;
-      const __nv_bfloat162 a2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-      const __nv_bfloat162 b2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-      *reinterpret_cast<uint2 *>(out + ((size_t)row * H + h) * KV4_DIM + 32 * b + 4 * u) =
-          make_uint2(*reinterpret_cast<const uint32_t *>(&a2),
-                     *reinterpret_cast<const uint32_t *>(&b2));
-    }
-    if (tid < H && lse)
-      lse[(size_t)row * H + tid] = cs[tid] == 0.f ? NEG : (cm[tid] + log2f(cs[tid])) * LN2;
-    return;
-  }
-  // The cluster: every CTA first sums its own warps (into the first warp's share, each
-  // value by the thread that read it), then finishes heads me, me + C, ...
-  float *own = reinterpret_cast<float *>(a4_smem);
-  for (int x = tid; x < H * (KV4_DIM / 4); x += WARPS * 32) {
-    const int h = x >> 5, at = h * A4_OSTRIDE + 4 * (x & 31);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < WARPS; w++) {
-      const float a = wm[w * NH + h];
-      const float4 v = *reinterpret_cast<const float4 *>(
-          reinterpret_cast<const float *>(a4_smem + w * RING) + at);
-      acc.x = fmaf(a, v.x, acc.x);
-      acc.y = fmaf(a, v.y, acc.y);
-      acc.z = fmaf(a, v.z, acc.z);
-      acc.w = fmaf(a, v.w, acc.w);
-    }
-    *reinterpret_cast<float4 *>(own + at) = acc;
-  }
-  cl.sync();
-  const int nloc = me < H ? (H - me + C - 1) / C : 0;
-  for (int x = tid; x < nloc * C; x += WARPS * 32) {
-    const int i = x / C, r = x - i * C, h = me + C * i;
-    xm[i * A4_MAX_CLUSTER + r] = cl.map_shared_rank(cm, r)[h];
-    xl[i * A4_MAX_CLUSTER + r] = cl.map_shared_rank(cs, r)[h];
-  }
-  __syncthreads();
-  if (tid < nloc) {
-    float mx = NEG, sum = 0.f;
-    for (int r = 0; r < C; r++) mx = fmaxf(mx, xm[tid * A4_MAX_CLUSTER + r]);
-    for (int r = 0; r < C; r++) {
-      const float mr = xm[tid * A4_MAX_CLUSTER + r], lr = xl[tid * A4_MAX_CLUSTER + r];
-      const float a = lr != lr ? lr : mr == NEG ? 0.f : ex2(mr - mx);
-      xm[tid * A4_MAX_CLUSTER + r] = a;
-      sum += lr != lr ? lr : a * lr;
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    for (int r = 0; r < C; r++) xm[tid * A4_MAX_CLUSTER + r] *= inv;
-    if (lse)
-      lse[(size_t)row * H + me + C * tid] = sum == 0.f ? NEG : (mx + log2f(sum)) * LN2;
-  }
-  __syncthreads();
-  for (int x = tid; x < nloc * (KV4_DIM / 4); x += WARPS * 32) {
-    const int i = x >> 5, h = me + C * i, b = (x >> 3) & 3, u = x & 7;
-    const int at = h * A4_OSTRIDE + 32 * b + 4 * (u ^ (2 * b));
-    float4 part[A4_MAX_CLUSTER];
-#pragma unroll
-    for (int r = 0; r < A4_MAX_CLUSTER; r++)
-      if (r < C) part[r] = *reinterpret_cast<const float4 *>(cl.map_shared_rank(own, r) + at);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int r = 0; r < A4_MAX_CLUSTER; r++)
-      if (r < C) {
-        const float a = xm[i * A4_MAX_CLUSTER + r];
-        acc.x = fmaf(a, part[r].x, acc.x);
-        acc.y = fmaf(a, part[r].y, acc.y);
-        acc.z = fmaf(a, part[r].z, acc.z);
-        acc.w = fmaf(a, part[r].w, acc.w);
-      }
-    const __nv_bfloat162 a2 = __floats2bfloat162_rn(acc.x, acc.y);
-    const __nv_bfloat162 b2 = __floats2bfloat162_rn(acc.z, acc.w);
-    *reinterpret_cast<uint2 *>(out + ((size_t)row * H + h) * KV4_DIM + 32 * b + 4 * u) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&a2),
-                   *reinterpret_cast<const uint32_t *>(&b2));
-  }
-  cl.sync();  // no CTA leaves while another reads its shared memory
-}
-
-template <int MT, int WARPS>
-static cudaError_t launch_attn_kv4_as(const uint16_t *q, const uint8_t *kv4,
-                                      const uint8_t *kv4_scale, const int32_t *idx,
-                                      const int32_t *cu_q, const int32_t *cu_k, int S, int total_q,
-                                      int H, int topk, float scale, int C, uint16_t *out,
-                                      float *lse, int *status, cudaStream_t st) {
-  static std::atomic<int> attr[64];
-  constexpr size_t smem = A4Smem<MT>::bytes(WARPS);
-  static_assert(smem <= 232448, "a CTA's shared memory");
-  const void *fn = (const void *)attn_kv4_kernel<MT, WARPS>;
-  cudaError_t e = set_smem_once(fn, smem, attr);
-  if (e != cudaSuccess) return e;
-  const int steps = (topk + A4_STEP - 1) / A4_STEP;
-  const int per = (steps + C - 1) / C * A4_STEP;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)total_q * C);
-  cfg.blockDim = dim3(WARPS * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attrs[1];
-  attrs[0].id = cudaLaunchAttributeClusterDimension;
-  attrs[0].val.clusterDim.x = C;
-  attrs[0].val.clusterDim.y = 1;
-  attrs[0].val.clusterDim.z = 1;
-  cfg.attrs = attrs;
-  cfg.numAttrs = 1;
-  ProfScope ps(K_ATTENTION_KV4, st);
-  return cudaLaunchKernelEx(&cfg, attn_kv4_kernel<MT, WARPS>, q, kv4, kv4_scale, idx, cu_q, cu_k,
-                            S, H, topk, per, scale, out, lse, status);
-}
-
-cudaError_t launch_attention_kv4(const uint16_t *q, const uint8_t *kv4, const uint8_t *kv4_scale,
-                                 const int32_t *idx, const int32_t *cu_q, const int32_t *cu_k,
-                                 int S, int total_q, int H, int topk, float scale, uint16_t *out,
-                                 float *lse, int num_sms, int *status, cudaStream_t st) {
-  // A row is split over the CTAs of a cluster while the rows alone leave SMs idle and
-  // every CTA still has a step for each of its warps.
-  int C = 1;
-  while (C < A4_MAX_CLUSTER && total_q * C * 2 <= num_sms && topk >= C * 2 * 4 * A4_STEP) C *= 2;
-  if (H <= 16)
-    return launch_attn_kv4_as<1, 4>(q, kv4, kv4_scale, idx, cu_q, cu_k, S, total_q, H, topk, scale,
-                                    C, out, lse, status, st);
-  return launch_attn_kv4_as<2, 4>(q, kv4, kv4_scale, idx, cu_q, cu_k, S, total_q, H, topk, scale,
-                                  C, out, lse, status, st);
-}
-
-// ---------------------------------------------------------------------------
-// Token weights: the scores again, against the row's log-sum-exp.  A warp takes 32 tokens
-// at a time; sum_h 2^(x - lse) of every token ends in one lane, which adds it to the
-// token's accumulator as a whole multiple of 2^-32: integer sums do not depend on the
-// order in which the rows arrive.
-
-constexpr int TW_WARPS = 4;
 
 // Sum over the 8 lanes g of a column c: v[i] (i = 0..7) -> the sum of v[g].
 __device__ __forceinline__ float column_sum(float (&v)[8], int g) {
@@ -615,21 +355,10 @@ __device__ __forceinline__ float column_sum(float (&v)[8], int g) {
   return v[0];
 }
 
-// Adds the weights of a step's 32 tokens: x = scores in powers of two, fl = the heads'
-// log-sum-exps in powers of two (+inf: the head adds nothing).
-template <int MT>
-__device__ __forceinline__ void add_weights(const float (&x)[MT][4][4], const float (&fl)[MT][2],
-                                            int tok, size_t kbase, int lane,
-                                            unsigned long long *weights, int *status) {
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; i++) {
-    v[i] = 0.f;
-#pragma unroll
-    for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-      for (int r = 0; r < 2; r++) v[i] += ex2(x[mt][i >> 1][2 * r + (i & 1)] - fl[mt][r]);
-  }
+// Adds the weights of a step's 32 tokens (tok: lane t's is token t, -1 = none).  v[i] = this
+// lane's heads' sum for column i & 1 of tile i >> 1.
+__device__ __forceinline__ void add_weights(float (&v)[8], int tok, unsigned long long *weights,
+                                            int lane, int *status) {
   const float w = column_sum(v, lane >> 2);
   // lane (g, c) holds value g of column pair c: token 8 (g / 2) + 2c + g % 2
   const int g = lane >> 2, c = lane & 3;
@@ -640,103 +369,768 @@ __device__ __forceinline__ void add_weights(const float (&x)[MT][4][4], const fl
     return;
   }
   const unsigned long long fx = __float2ull_rn(w * 4294967296.f);
-  if (fx) atomicAdd(weights + kbase + (size_t)j, fx);
+  if (fx) atomicAdd(weights + j, fx);
 }
 
+// Factor of a share with maximum m and sum l in a merge whose maximum is mx: 0 for a share
+// of no score; a share that holds a NaN keeps it whatever its maximum says.
+__device__ __forceinline__ float share_factor(float m, float l, float mx) {
+  return l != l ? l : m == -__int_as_float(0x7f800000) ? 0.f : ex2(m - mx);
+}
+
+__device__ __forceinline__ void add_share(float4 &acc, float a, const float4 &v) {
+  acc.x = fmaf(a, v.x, acc.x);
+  acc.y = fmaf(a, v.y, acc.y);
+  acc.z = fmaf(a, v.z, acc.z);
+  acc.w = fmaf(a, v.w, acc.w);
+}
+
+// four values of head h's partial output, summed over W warps
+template <int W>
+__device__ __forceinline__ float4 sum_shares(const uint8_t *smem, int ring, const float *factor,
+                                             int NH, int h, int at) {
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < W; w++)
+    add_share(acc, factor[w * NH + h],
+              *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + w * ring) +
+                                                at));
+  return acc;
+}
+
+__device__ __forceinline__ void store_out(uint16_t *dst, const float4 &v, float by) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * by, v.y * by);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.z * by, v.w * by);
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
+                                               *reinterpret_cast<const uint32_t *>(&b));
+}
+
+// A warp's running state over its tokens: unnormalised outputs, reference maxima (in
+// exponents of two) and sums of its 16-head tiles.
 template <int MT>
-__global__ void __launch_bounds__(TW_WARPS * 32)
-token_weights_kv4_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict__ kv4,
-                         const uint8_t *__restrict__ kv4_scale, const int32_t *__restrict__ idx,
-                         const float *__restrict__ lse, const int32_t *__restrict__ cu_q,
-                         const int32_t *__restrict__ cu_k, int S, int H, int topk, float scale,
-                         unsigned long long *__restrict__ weights, int *status) {
-  extern __shared__ __align__(16) uint8_t a4_smem[];
-  constexpr int NST = 3;
-  const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int s = find_seq(cu_q, S, row);
-  const int kbase = __ldg(cu_k + s);
-  Ring<NST> ring;
-  ring.e0 = 0;
-  ring.e1 = topk;
-  const int steps = (topk + A4_STEP - 1) / A4_STEP;
-  ring.irow = idx + (size_t)row * topk;
-  ring.first = blockIdx.y * TW_WARPS + warp;
-  ring.stride = gridDim.y * TW_WARPS;
-  ring.nsteps = steps > ring.first ? (steps - ring.first + ring.stride - 1) / ring.stride : 0;
-  ring.kcap = __ldg(cu_k + s + 1) - kbase;
-  ring.kbase = (size_t)kbase;
-  ring.kv4 = kv4;
-  ring.kv4_scale = kv4_scale;
-  ring.ring = a4_smem + warp * NST * A4_STAGE;
-  ring.lane = lane;
-  ring.start();
-  QFrags<MT> qf;
-  float f[MT][2], fl[MT][2];
-  if constexpr (MT == 1) {
-    load_q_frags(q, (size_t)row, H, 0, lane, qf.f, f[0]);
-  } else {
-    uint4 *sq = reinterpret_cast<uint4 *>(a4_smem + TW_WARPS * NST * A4_STAGE);
-    qf.s = sq;
-    qf.lane = lane;
+struct Running {
+  float o[MT][16][4];
+  float m[MT][2];   // -inf before the first step, and only then
+  float2 l[MT][2];  // sums of the even and of the odd columns
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int mt = 0; mt < MT; mt++) {
-      uint32_t t[8][4];
-      load_q_frags(q, (size_t)row, H, mt, lane, t, f[mt]);
 #pragma unroll
-      for (int ks = 0; ks < 8; ks++)
-        if ((mt * 8 + ks) % TW_WARPS == warp)
-          sq[(mt * 8 + ks) * 32 + lane] = make_uint4(t[ks][0], t[ks][1], t[ks][2], t[ks][3]);
+      for (int t = 0; t < 16; t++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) o[mt][t][e] = 0.f;
+#pragma unroll
+      for (int r = 0; r < 2; r++) {
+        m[mt][r] = -__int_as_float(0x7f800000);
+        l[mt][r] = make_float2(0.f, 0.f);
+      }
     }
-    __syncthreads();
   }
-#pragma unroll
-  for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-    for (int r = 0; r < 2; r++) {
-      f[mt][r] *= scale * LOG2E;
-      const int h = 16 * mt + (lane >> 2) + 8 * r;
-      const float v = h < H ? __ldg(lse + (size_t)row * H + h) : -__int_as_float(0x7f800000);
-      // a head of no index (or past the last) has no weights
-      fl[mt][r] = v == -__int_as_float(0x7f800000) ? -v : v * LOG2E;
-    }
+  // the sum of a head over the quad's columns
+  __device__ __forceinline__ float total(int mt, int r) const {
+    float sum = l[mt][r].x + l[mt][r].y;
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    return sum + __shfl_xor_sync(0xffffffffu, sum, 2);
+  }
+};
+
+// All steps of a warp's ring.  KEEP: the raw scores go to `scores` (this lane's place), one
+// step's after another's `step_scores` further on.
+template <int MT, bool KEEP, typename R>
+__device__ __forceinline__ void attend(R &ring, const LanePlaces &lp, const uint4 *qf,
+                                       const float (&f)[MT][2], int lane, Running<MT> &st,
+                                       float4 *scores, int step_scores) {
+  const float NEG = -__int_as_float(0x7f800000);
+  const int c = lane & 3;
+  const uint32_t magic = kv4_magic();
+  auto &o = st.o;
+  auto &m = st.m;
+  auto &l = st.l;
   for (int n = 0; n < ring.nsteps; n++) {
     uint32_t valid;
-    int tok = ring.token(n);
-    if (tok >= ring.kcap) tok = -1;
-    const uint8_t *stage = ring.arrive(n, valid);
+    const uint8_t *stage = ring.arrive(lp, lane, valid);
     if (!valid) continue;
     float x[MT][4][4];
-    kv4_scores<MT>(stage, qf, lane, x);
+#pragma unroll
+    for (int j = 0; j < 4; j++) kv4_scores(stage, j, lp, qf, magic, x);
+    if (KEEP) {
+#pragma unroll
+      for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          scores[(size_t)n * step_scores + (mt * 4 + j) * 32] =
+              make_float4(x[mt][j][0], x[mt][j][1], x[mt][j][2], x[mt][j][3]);
+    }
+    // exponents against the reference maxima; -inf where there is no token
+    float top = NEG;
+    float y[MT][4][4];
 #pragma unroll
     for (int mt = 0; mt < MT; mt++)
 #pragma unroll
       for (int j = 0; j < 4; j++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) x[mt][j][e] *= f[mt][e >> 1];
-    add_weights<MT>(x, fl, tok, (size_t)kbase, lane, weights, status);
+        for (int r = 0; r < 2; r++) {
+          const float2 t = fma2(make_float2(x[mt][j][2 * r], x[mt][j][2 * r + 1]), f[mt][r],
+                                -m[mt][r]);
+          y[mt][j][2 * r] = t.x;
+          y[mt][j][2 * r + 1] = t.y;
+        }
+    if (valid != 0xffffffffu) {
+      const uint32_t v = valid >> (2 * c);
+#pragma unroll
+      for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            if (!((v >> (8 * j + (e & 1))) & 1u)) y[mt][j][e] = NEG;
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) top = fmaxf(top, y[mt][j][e]);
+    // the reference maxima rise (and sums and outputs are rescaled) only where a score
+    // exceeds one by 2^TAU; a first score always does
+    if (__any_sync(0xffffffffu, top > A4_TAU)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+          float mx = m[mt][r];
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int e = 2 * r; e < 2 * r + 2; e++)
+              if (y[mt][j][e] != NEG) mx = fmaxf(mx, x[mt][j][e] * f[mt][r]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float a = mx == NEG ? 1.f : ex2(m[mt][r] - mx);
+          m[mt][r] = mx;
+          l[mt][r].x *= a;
+          l[mt][r].y *= a;
+#pragma unroll
+          for (int t = 0; t < 16; t++) {
+            o[mt][t][2 * r] *= a;
+            o[mt][t][2 * r + 1] *= a;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int e = 2 * r; e < 2 * r + 2; e++)
+              if (y[mt][j][e] != NEG) y[mt][j][e] = fmaf(x[mt][j][e], f[mt][r], -mx);
+        }
+    }
+    uint32_t p[MT][4][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+      for (int r = 0; r < 2; r++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const float2 pp = make_float2(ex2(y[mt][j][2 * r]), ex2(y[mt][j][2 * r + 1]));
+          l[mt][r] = add2(l[mt][r], pp);
+          p[mt][j][r] = as_u32(__floats2half2_rn(pp.x, pp.y));
+        }
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      ValueRaw r;
+      r.load(stage, i, lp);
+      kv4_values<MT>(r, i, 0, p, magic, o);
+      kv4_values<MT>(r, i, 1, p, magic, o);
+    }
   }
   cp_async_wait_all();
-  if (__any_sync(0xffffffffu, ring.bad) && lane == 0) raise_status(status, HISA_ERR_INVALID_ARG);
+  __syncwarp();  // the ring is free
 }
 
-// The same for bf16 keys.  Lane (g, c) takes dimensions 32c .. 32c + 31 of token g of
-// every 8 straight from memory (64 bytes): fragment w holds the pairs of its 8-dimension
-// word w, as does the query's.
+// Heads past the last, and those of a row without tokens, have no weights.
 template <int MT>
-__global__ void __launch_bounds__(TW_WARPS * 32)
+__device__ __forceinline__ void dead_heads(int H, int g, float (&f)[MT][2], float (&m)[MT][2],
+                                           float (&inv)[MT][2]) {
+#pragma unroll
+  for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+    for (int r = 0; r < 2; r++)
+      if (16 * mt + g + 8 * r >= H || m[mt][r] == -__int_as_float(0x7f800000))
+        f[mt][r] = m[mt][r] = inv[mt][r] = 0.f;
+}
+
+// v += sum over the lane's heads of 2^(x f - m) / l of a step's scores
+template <int MT>
+__device__ __forceinline__ void weigh_step(int mt, int j, const float4 &t, const float (&f)[MT][2],
+                                           const float (&m)[MT][2], const float (&inv)[MT][2],
+                                           float (&v)[8]) {
+  v[2 * j] = fmaf(ex2(fmaf(t.x, f[mt][0], -m[mt][0])), inv[mt][0], v[2 * j]);
+  v[2 * j + 1] = fmaf(ex2(fmaf(t.y, f[mt][0], -m[mt][0])), inv[mt][0], v[2 * j + 1]);
+  v[2 * j] = fmaf(ex2(fmaf(t.z, f[mt][1], -m[mt][1])), inv[mt][1], v[2 * j]);
+  v[2 * j + 1] = fmaf(ex2(fmaf(t.w, f[mt][1], -m[mt][1])), inv[mt][1], v[2 * j + 1]);
+}
+
+// The weights of a warp's tokens from a second look at their keys; m, inv: the row's
+// maxima and inverse sums.
+template <int MT, typename R>
+__device__ __forceinline__ void weigh_again(R &ring, const LanePlaces &lp, const uint4 *qf,
+                                            const float (&f)[MT][2], const float (&m)[MT][2],
+                                            const float (&inv)[MT][2], int lane,
+                                            unsigned long long *weights, int *status) {
+  const uint32_t magic = kv4_magic();
+  ring.start(lp, lane);
+  const int32_t *entry = ring.irow + ring.first_e;
+  for (int n = 0; n < ring.nsteps; n++) {
+    uint32_t valid;
+    const uint8_t *stage = ring.arrive(lp, lane, valid);
+    if (!valid) continue;
+    const int tok = (valid >> lane) & 1u ? __ldg(entry + (size_t)n * ring.stride) : -1;
+    float x[MT][4][4], v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      kv4_scores(stage, j, lp, qf, magic, x);
+#pragma unroll
+      for (int mt = 0; mt < MT; mt++)
+        weigh_step<MT>(mt, j, make_float4(x[mt][j][0], x[mt][j][1], x[mt][j][2], x[mt][j][3]), f,
+                       m, inv, v);
+    }
+    add_weights(v, tok, weights, lane, status);
+  }
+  cp_async_wait_all();
+}
+
+// A warp's partial output to its ring, [head][dimension] with the 4-value pieces of a
+// 32-dimension block turned by the block so that the lanes' stores spread over the banks;
+// its maxima and sums to wm and wl.
+template <int MT>
+__device__ __forceinline__ void store_share(const Running<MT> &st, uint8_t *ring, float *wm,
+                                            float *wl, int lane) {
+  const int g = lane >> 2, c = lane & 3;
+  float *po = reinterpret_cast<float *>(ring);
+#pragma unroll
+  for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+    for (int r = 0; r < 2; r++) {
+      const float sum = st.total(mt, r);
+      const int h = 16 * mt + g + 8 * r;
+      if (c == 0) {
+        wm[h] = st.m[mt][r];
+        wl[h] = sum;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; u++) {
+        // piece u of dimensions 32c ..: tiles 4 (u & 3) .., column 2c + (u >> 2)
+        const int e = 2 * r + (u >> 2), t = 4 * (u & 3);
+        *reinterpret_cast<float4 *>(po + h * A4_OSTRIDE + 32 * c + 4 * (u ^ (2 * c))) =
+            make_float4(st.o[mt][t][e], st.o[mt][t + 1][e], st.o[mt][t + 2][e],
+                        st.o[mt][t + 3][e]);
+      }
+    }
+}
+
+// Maxima and sums of W warps' shares of head h: their factors replace the maxima in wm.
+template <int W>
+__device__ __forceinline__ void join_shares(float *wm, const float *wl, int NH, int h, float &mx,
+                                            float &sum) {
+  mx = -__int_as_float(0x7f800000);
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < W; w++) mx = fmaxf(mx, wm[w * NH + h]);
+#pragma unroll
+  for (int w = 0; w < W; w++) {
+    const float lw = wl[w * NH + h], a = share_factor(wm[w * NH + h], lw, mx);
+    wm[w * NH + h] = a;
+    sum += lw != lw ? lw : a * lw;
+  }
+}
+
+__device__ __forceinline__ float inverse_sum(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+__device__ __forceinline__ float lse_of(float mx, float sum) {
+  return sum == 0.f ? -__int_as_float(0x7f800000) : (mx + log2f(sum)) * LN2;
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: W = 1 or 2 warps per row, so that a row's start and end (about 3000 cycles of
+// latency) hide behind the other warps of the SM and, for one warp, nothing is merged.
+
+template <int MT>
+constexpr size_t rows_smem(int W) {
+  return (size_t)A4_WARPS * a4_ring(MT) + (size_t)(A4_WARPS / W) * MT * 4096 +
+         (size_t)A4_WARPS * 16 * MT * 8;
+}
+
+template <int ID, int N>
+__device__ __forceinline__ void asm_bar() {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory");
+}
+template <int W>
+__device__ __forceinline__ void sync_row(int group) {
+  static_assert(W <= 2, "two rows of two warps");
+  if (W == 1)
+    __syncwarp();
+  else
+    group ? asm_bar<2, W * 32>() : asm_bar<1, W * 32>();
+}
+
+template <int MT, int W, bool WT>
+__global__ void __launch_bounds__(A4_THREADS, a4_ctas(MT))
+attn_kv4_rows_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict__ kv4,
+                     const uint8_t *__restrict__ kv4_scale, const int32_t *__restrict__ idx,
+                     const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, int S,
+                     int total_q, int H, int topk, float scale, uint16_t *__restrict__ out,
+                     float *__restrict__ lse, unsigned long long *__restrict__ weights,
+                     int *status) {
+  extern __shared__ __align__(16) uint8_t a4_smem[];
+  constexpr int NST = a4_stages(MT), RING = a4_ring(MT), NH = 16 * MT;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = warp / W, part = warp % W;
+  const int row = blockIdx.x * (A4_WARPS / W) + group;
+  if (row >= total_q) return;  // all of the row's warps
+  const int g = lane >> 2, c = lane & 3;
+  uint4 *qs = reinterpret_cast<uint4 *>(a4_smem + A4_WARPS * RING + group * MT * 4096);
+  float *wm = reinterpret_cast<float *>(a4_smem + A4_WARPS * RING +
+                                        (A4_WARPS / W) * MT * 4096) + group * 2 * W * NH;
+  float *wl = wm + W * NH;
+  uint8_t *mem = a4_smem + warp * RING;
+
+  const int s = find_seq(cu_q, S, row);
+  const int kbase = __ldg(cu_k + s), kcap = __ldg(cu_k + s + 1) - kbase;
+  const LanePlaces lp(lane);
+  const int32_t *irow = idx + (size_t)row * topk;
+  Ring<NST, NST - 1, true> ring;
+  ring.init(irow, 0, topk, part, W, kbase, kcap, kv4, kv4_scale, mem, lane);
+  ring.start(lp, lane);
+  float f[MT][2];
+  load_query<MT, W>(q, (size_t)row, H, scale, qs, lane, part, f);
+  sync_row<W>(group);
+  const uint4 *qf = qs + lane;
+  Running<MT> st;
+  st.clear();
+  attend<MT, false>(ring, lp, qf, f, lane, st, nullptr, 0);
+  if (__any_sync(0xffffffffu, ring.bad) && lane == 0) raise_status(status, HISA_ERR_INVALID_ARG);
+
+  float mx[MT][2], inv[MT][2];  // of the row (W = 1), for the outputs and the weights
+  if (W == 1) {
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+      for (int r = 0; r < 2; r++) {
+        const int h = 16 * mt + g + 8 * r;
+        const float sum = st.total(mt, r);
+        mx[mt][r] = st.m[mt][r];
+        inv[mt][r] = inverse_sum(sum);
+        if (h >= H) continue;
+        if (c == 0 && lse) lse[(size_t)row * H + h] = lse_of(mx[mt][r], sum);
+        // the lane's 32 dimensions: 16 of column 2c, 16 of column 2c + 1
+        uint4 *dst = reinterpret_cast<uint4 *>(out + ((size_t)row * H + h) * KV4_DIM + 32 * c);
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int t = 8 * (u & 1) + 2 * i, e = 2 * r + (u >> 1);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(st.o[mt][t][e] * inv[mt][r],
+                                                           st.o[mt][t + 1][e] * inv[mt][r]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+          }
+          dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+  } else {
+    store_share<MT>(st, mem, wm + part * NH, wl + part * NH, lane);
+    sync_row<W>(group);
+    // every thread of the row finishes some pieces; the factors it needs it works out
+    // itself, and the row's maxima and inverse sums of its fragments' heads
+    const uint8_t *shares = a4_smem + group * W * RING;
+    for (int x = part * 32 + lane; x < H * (KV4_DIM / 4); x += W * 32) {
+      const int h = x >> 5, b = (x >> 3) & 3, u = x & 7;
+      float top = -__int_as_float(0x7f800000), sum = 0.f, a[W];
+#pragma unroll
+      for (int w = 0; w < W; w++) top = fmaxf(top, wm[w * NH + h]);
+#pragma unroll
+      for (int w = 0; w < W; w++) {
+        const float lw = wl[w * NH + h];
+        a[w] = share_factor(wm[w * NH + h], lw, top);
+        sum += lw != lw ? lw : a[w] * lw;
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < W; w++)
+        add_share(acc, a[w],
+                  *reinterpret_cast<const float4 *>(
+                      reinterpret_cast<const float *>(shares + w * RING) + h * A4_OSTRIDE +
+                      32 * b + 4 * (u ^ (2 * b))));
+      store_out(out + ((size_t)row * H + h) * KV4_DIM + 32 * b + 4 * u, acc, inverse_sum(sum));
+      if (lse && (x & 31) == 0) lse[(size_t)row * H + h] = lse_of(top, sum);
+    }
+    if (WT) {
+#pragma unroll
+      for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+          const int h = 16 * mt + g + 8 * r;
+          float top = -__int_as_float(0x7f800000), sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < W; w++) top = fmaxf(top, wm[w * NH + h]);
+#pragma unroll
+          for (int w = 0; w < W; w++) {
+            const float lw = wl[w * NH + h];
+            sum += lw != lw ? lw : share_factor(wm[w * NH + h], lw, top) * lw;
+          }
+          mx[mt][r] = top;
+          inv[mt][r] = inverse_sum(sum);
+        }
+      sync_row<W>(group);  // the shares are read: the rings take keys again
+    }
+  }
+  if (WT) {
+    dead_heads<MT>(H, g, f, mx, inv);
+    Ring<NST, NST - 1, false> again;
+    again.init(irow, 0, topk, part, W, kbase, kcap, kv4, kv4_scale, mem, lane);
+    weigh_again<MT>(again, lp, qf, f, mx, inv, lane, weights + kbase, status);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: the four warps of a CTA, and the C CTAs of a cluster, share a row.
+
+template <int MT>
+struct SplitSmem {
+  static constexpr int QBYTES = MT * 4096;
+  static constexpr int NH = 16 * MT;
+  // ring of every warp | query fragments | m, l of every warp and head | m, l of the CTA |
+  // merge factors of the cluster | scores (weights only, one step's 32 tokens after another)
+  static constexpr size_t bytes = (size_t)A4_WARPS * a4_ring(MT) + QBYTES +
+                                  (size_t)A4_WARPS * NH * 8 + (size_t)NH * 8 +
+                                  (size_t)NH * A4_MAX_CLUSTER * 4;
+  static constexpr size_t STEP_SCORES = (size_t)A4_STEP * NH * 4;
+};
+
+template <int MT, bool WT>
+__global__ void __launch_bounds__(A4_THREADS, a4_ctas(MT))
+attn_kv4_split_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict__ kv4,
+                      const uint8_t *__restrict__ kv4_scale, const int32_t *__restrict__ idx,
+                      const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, int S,
+                      int H, int topk, int per_cta, float scale, uint16_t *__restrict__ out,
+                      float *__restrict__ lse, unsigned long long *__restrict__ weights,
+                      int *status) {
+  extern __shared__ __align__(16) uint8_t a4_smem[];
+  constexpr int NST = a4_stages(MT), RING = a4_ring(MT), NH = 16 * MT;
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = (int)cl.num_blocks(), me = (int)cl.block_rank();
+  const int row = blockIdx.x / C;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2;
+  const float NEG = -__int_as_float(0x7f800000);
+  uint8_t *qs = a4_smem + A4_WARPS * RING;
+  float *wm = reinterpret_cast<float *>(qs + SplitSmem<MT>::QBYTES);  // [warps][NH]
+  float *wl = wm + A4_WARPS * NH;                                     // [warps][NH]
+  float *cm = wl + A4_WARPS * NH, *cs = cm + NH;  // the CTA's maximum and sum per head
+  float *xm = cs + NH;                            // factors of the cluster's CTAs [NH][C]
+  // scores of this warp's steps: the lane that wrote a value reads it back
+  constexpr int STEP = (int)(SplitSmem<MT>::STEP_SCORES / 16);
+  float4 *scores = reinterpret_cast<float4 *>(xm + NH * A4_MAX_CLUSTER) + warp * STEP + lane;
+
+  const int s = find_seq(cu_q, S, row);
+  const int kbase = __ldg(cu_k + s), kcap = __ldg(cu_k + s + 1) - kbase;
+  const LanePlaces lp(lane);
+  const int e0 = me * per_cta, e1 = min(topk, e0 + per_cta);
+  const int32_t *irow = idx + (size_t)row * topk;
+  uint8_t *mem = a4_smem + warp * RING;
+  Ring<NST, NST - 1, true> ring;
+  ring.init(irow, e0, e1, warp, A4_WARPS, kbase, kcap, kv4, kv4_scale, mem, lane);
+  ring.start(lp, lane);
+  float f[MT][2];
+  load_query<MT, A4_WARPS>(q, (size_t)row, H, scale, reinterpret_cast<uint4 *>(qs), lane, warp, f);
+  __syncthreads();
+  const uint4 *qf = reinterpret_cast<const uint4 *>(qs) + lane;
+  Running<MT> st;
+  st.clear();
+  attend<MT, WT>(ring, lp, qf, f, lane, st, scores, A4_WARPS * STEP);
+  if (__any_sync(0xffffffffu, ring.bad) && lane == 0) raise_status(status, HISA_ERR_INVALID_ARG);
+  store_share<MT>(st, mem, wm + warp * NH, wl + warp * NH, lane);
+  __syncthreads();
+  if (tid < NH) join_shares<A4_WARPS>(wm, wl, NH, tid, cm[tid], cs[tid]);
+  __syncthreads();
+  // With several CTAs every one sums its own warps first (into the first warp's share, each
+  // value by the thread that read it) and learns the others' maxima and sums; CTA me then
+  // finishes the heads me, me + C, ...
+  float *own = reinterpret_cast<float *>(a4_smem);
+  if (C > 1) {
+    for (int x = tid; x < H * (KV4_DIM / 4); x += A4_THREADS) {
+      const int h = x >> 5, at = h * A4_OSTRIDE + 4 * (x & 31);
+      *reinterpret_cast<float4 *>(own + at) = sum_shares<A4_WARPS>(a4_smem, RING, wm, NH, h, at);
+    }
+    cl.sync();
+    if (tid < H) {
+      float mr[A4_MAX_CLUSTER], lr[A4_MAX_CLUSTER], mx = NEG, sum = 0.f;
+#pragma unroll
+      for (int r = 0; r < A4_MAX_CLUSTER; r++) {
+        mr[r] = r < C ? cl.map_shared_rank(cm, r)[tid] : NEG;
+        lr[r] = r < C ? cl.map_shared_rank(cs, r)[tid] : 0.f;
+        mx = fmaxf(mx, mr[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < A4_MAX_CLUSTER; r++) {
+        mr[r] = share_factor(mr[r], lr[r], mx);
+        if (r < C) sum += lr[r] != lr[r] ? lr[r] : mr[r] * lr[r];
+      }
+      const float inv = inverse_sum(sum);
+#pragma unroll
+      for (int r = 0; r < A4_MAX_CLUSTER; r++)
+        if (r < C) xm[tid * A4_MAX_CLUSTER + r] = mr[r] * inv;
+      if (lse && tid % C == me) lse[(size_t)row * H + tid] = lse_of(mx, sum);
+      wm[tid] = mx;  // the warps' factors are not needed any more
+      wl[tid] = inv;
+    }
+    __syncthreads();
+    const int nloc = me < H ? (H - me + C - 1) / C : 0;
+    for (int x = tid; x < nloc * (KV4_DIM / 4); x += A4_THREADS) {
+      const int h = me + C * (x >> 5), b = (x >> 3) & 3, u = x & 7;
+      const int at = h * A4_OSTRIDE + 32 * b + 4 * (u ^ (2 * b));
+      float4 part[A4_MAX_CLUSTER];
+#pragma unroll
+      for (int r = 0; r < A4_MAX_CLUSTER; r++)
+        if (r < C) part[r] = *reinterpret_cast<const float4 *>(cl.map_shared_rank(own, r) + at);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < A4_MAX_CLUSTER; r++)
+        if (r < C) add_share(acc, xm[h * A4_MAX_CLUSTER + r], part[r]);
+      store_out(out + ((size_t)row * H + h) * KV4_DIM + 32 * b + 4 * u, acc, 1.f);
+    }
+  } else {
+    for (int x = tid; x < H * (KV4_DIM / 4); x += A4_THREADS) {
+      const int h = x >> 5, b = (x >> 3) & 3, u = x & 7;
+      const float4 acc = sum_shares<A4_WARPS>(a4_smem, RING, wm, NH, h,
+                                              h * A4_OSTRIDE + 32 * b + 4 * (u ^ (2 * b)));
+      store_out(out + ((size_t)row * H + h) * KV4_DIM + 32 * b + 4 * u, acc, inverse_sum(cs[h]));
+    }
+    if (tid < H && lse) lse[(size_t)row * H + tid] = lse_of(cm[tid], cs[tid]);
+    if (WT) {
+      __syncthreads();
+      if (tid < H) {
+        wm[tid] = cm[tid];
+        wl[tid] = inverse_sum(cs[tid]);
+      }
+      __syncthreads();
+    }
+  }
+  // The weights: the scores are there, the row's maxima and sums known.
+  if (WT) {
+    float mx[MT][2], inv[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+      for (int r = 0; r < 2; r++) {
+        mx[mt][r] = wm[16 * mt + g + 8 * r];
+        inv[mt][r] = wl[16 * mt + g + 8 * r];
+      }
+    dead_heads<MT>(H, g, f, mx, inv);
+    for (int n = 0; n < ring.nsteps; n++) {
+      const int e = e0 + (warp + n * A4_WARPS) * A4_STEP + lane;
+      int tok = e < e1 ? __ldg(irow + e) : -1;
+      if (tok >= kcap) tok = -1;
+      if (!__any_sync(0xffffffffu, tok >= 0)) continue;
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          weigh_step<MT>(mt, j, scores[(size_t)n * A4_WARPS * STEP + (mt * 4 + j) * 32], f, mx, inv,
+                         v);
+      add_weights(v, tok, weights + kbase, lane, status);
+    }
+  }
+  if (C > 1) cl.sync();  // no CTA leaves while another reads its shared memory
+}
+
+struct AttnArgs {
+  const uint16_t *q;
+  const uint8_t *kv4, *kv4_scale;
+  const int32_t *idx, *cu_q, *cu_k;
+  int S, total_q, H, topk;
+  float scale;
+  uint16_t *out;
+  float *lse;
+  unsigned long long *weights;
+  int *status;
+};
+
+template <int MT, int W, bool WT>
+static cudaError_t launch_rows(const AttnArgs &a, cudaStream_t st) {
+  static std::atomic<int> attr[64];
+  constexpr size_t smem = rows_smem<MT>(W);
+  static_assert((smem + 1024) * a4_ctas(MT) <= 233472, "the CTAs of an SM");
+  const auto fn = attn_kv4_rows_kernel<MT, W, WT>;
+  const cudaError_t e = set_smem_once((const void *)fn, smem, attr);
+  if (e != cudaSuccess) return e;
+  constexpr int per = A4_WARPS / W;
+  ProfScope ps(K_ATTENTION_KV4, st);
+  fn<<<(a.total_q + per - 1) / per, A4_THREADS, smem, st>>>(
+      a.q, a.kv4, a.kv4_scale, a.idx, a.cu_q, a.cu_k, a.S, a.total_q, a.H, a.topk, a.scale, a.out,
+      a.lse, a.weights, a.status);
+  return cudaGetLastError();
+}
+
+template <int MT, bool WT>
+static cudaError_t launch_split(const AttnArgs &a, int C, cudaStream_t st) {
+  static std::atomic<int> attr[64];
+  const int per = ((a.topk + A4_STEP - 1) / A4_STEP + C - 1) / C;
+  const size_t smem = SplitSmem<MT>::bytes + (WT ? per * SplitSmem<MT>::STEP_SCORES : 0);
+  constexpr size_t most =
+      SplitSmem<MT>::bytes + (WT ? A4_SCORE_TOKENS / A4_STEP * SplitSmem<MT>::STEP_SCORES : 0);
+  static_assert(most <= 232448, "a CTA's shared memory");
+  const auto fn = attn_kv4_split_kernel<MT, WT>;
+  const cudaError_t e = set_smem_once((const void *)fn, most, attr);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.total_q * C);
+  cfg.blockDim = dim3(A4_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attrs[1];
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = C;
+  attrs[0].val.clusterDim.y = 1;
+  attrs[0].val.clusterDim.z = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 1;
+  ProfScope ps(K_ATTENTION_KV4, st);
+  return cudaLaunchKernelEx(&cfg, fn, a.q, a.kv4, a.kv4_scale, a.idx, a.cu_q, a.cu_k, a.S, a.H,
+                            a.topk, per * A4_STEP, a.scale, a.out, a.lse, a.weights, a.status);
+}
+
+template <int MT, bool WT>
+static cudaError_t launch_attn(const AttnArgs &a, int num_sms, cudaStream_t st) {
+  const int steps = (a.topk + A4_STEP - 1) / A4_STEP;
+  // Few rows: a row is split over a CTA's warps, and over the CTAs of a cluster while that
+  // leaves SMs idle and every CTA has a step for each of its warps.
+  int C = 1;
+  while (C < A4_MAX_CLUSTER && a.total_q * C * 2 <= num_sms && steps >= C * 2 * A4_WARPS) C *= 2;
+  const bool kept = !WT || (steps + C - 1) / C * A4_STEP <= A4_SCORE_TOKENS;
+  // Estimated time in steps of a warp, with a start and end that cost about three: the rows
+  // spread over all warps, and half a row for the last wave's idle warps.
+  const int slots = num_sms * a4_ctas(MT) * A4_WARPS;
+  auto cost = [&](int W) {
+    const double row = (steps + W - 1) / W + 3.0;
+    return (double)a.total_q * W / slots * row + 0.5 * row;
+  };
+  if (kept && (C > 1 || (cost(4) < cost(2) && cost(4) < cost(1)))) return launch_split<MT, WT>(a, C, st);
+  return cost(2) < cost(1) ? launch_rows<MT, 2, WT>(a, st) : launch_rows<MT, 1, WT>(a, st);
+}
+
+cudaError_t launch_attention_kv4(const uint16_t *q, const uint8_t *kv4, const uint8_t *kv4_scale,
+                                 const int32_t *idx, const int32_t *cu_q, const int32_t *cu_k,
+                                 int S, int total_q, int H, int topk, float scale, uint16_t *out,
+                                 float *lse, int64_t *weights, int num_sms, int *status,
+                                 cudaStream_t st) {
+  const AttnArgs a = {q, kv4, kv4_scale, idx, cu_q, cu_k, S, total_q, H, topk, scale, out, lse,
+                      reinterpret_cast<unsigned long long *>(weights), status};
+  if (H <= 16)
+    return weights ? launch_attn<1, true>(a, num_sms, st) : launch_attn<1, false>(a, num_sms, st);
+  return weights ? launch_attn<2, true>(a, num_sms, st) : launch_attn<2, false>(a, num_sms, st);
+}
+
+// ---------------------------------------------------------------------------
+// Token weights of the bf16 cache: the scores again, against the row's log-sum-exp.  A warp
+// takes 32 tokens at a time; sum_h 2^(x - lse) of every token ends in one lane, which adds
+// it to the token's accumulator as a whole multiple of 2^-32: integer sums do not depend on
+// the order in which the rows arrive.
+
+constexpr int TW_WARPS = 4;
+
+// The heads' log-sum-exps of lane (g, c), negated and in powers of two, as a pair of fp32:
+// the rounding of a single one would move every weight of the row.  -inf (no weights) for
+// a head with no index and past the last.
+struct NegLse {
+  float hi, lo;
+};
+__device__ __forceinline__ NegLse neg_lse(const float *lse, size_t row, int H, int h) {
+  const float INF = __int_as_float(0x7f800000);
+  const float v = h < H ? __ldg(lse + row * H + h) : -INF;
+  NegLse n;
+  n.hi = v == -INF ? -INF : -v * LOG2E;
+  n.lo = v == -INF ? 0.f : fmaf(-v, LOG2E_LO, fmaf(-v, LOG2E, -n.hi));
+  return n;
+}
+
+// What scale * log2(e) loses as one fp32 number, relative to it.
+__device__ __forceinline__ float scale_rest(float scale) {
+  const float hi = scale * LOG2E;
+  return hi == 0.f ? 0.f : (fmaf(scale, LOG2E, -hi) + scale * LOG2E_LO) / hi;
+}
+
+// v[i] = sum over the lane's heads of 2^(x f - lse), x the score fragments of 32 tokens;
+// rest = scale_rest
+template <int MT>
+__device__ __forceinline__ void weigh(const float (&x)[MT][4][4], const float (&f)[MT][2],
+                                      float rest, const NegLse (&nl)[MT][2], float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    v[i] = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+      for (int r = 0; r < 2; r++) {
+        const float t = x[mt][i >> 1][2 * r + (i & 1)];
+        v[i] += ex2(fmaf(t, f[mt][r], nl[mt][r].hi) + fmaf(t, f[mt][r] * rest, nl[mt][r].lo));
+      }
+  }
+}
+
+// The rows (256 bytes) come through a ring as above: lane (g, c) takes the 16-byte chunks 4i + c of token g of every 8, chunk i being the fragments 2i
+// and 2i + 1, of the query alike.  The matrix unit cuts sums off instead of rounding them,
+// which in a chain of eight would lower every score by a few 2^-24 of itself and every
+// weight by that times the score; so pairs are summed there and the four sums here.
+constexpr int TWB_STAGES = 3, TWB_ROW = KV4_DIM * 2, TWB_STAGE = A4_STEP * TWB_ROW;
+
+template <int MT>
+__global__ void __launch_bounds__(TW_WARPS * 32, 2)
 token_weights_kernel(const uint16_t *__restrict__ q, const uint16_t *__restrict__ k,
                      const int32_t *__restrict__ idx, const float *__restrict__ lse,
                      const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, int S,
                      int H, int topk, float scale, unsigned long long *__restrict__ weights,
                      int *status) {
+  extern __shared__ __align__(16) uint8_t a4_smem[];
   const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   const int s = find_seq(cu_q, S, row);
   const int kbase = __ldg(cu_k + s), kcap = __ldg(cu_k + s + 1) - kbase;
   const int32_t *irow = idx + (size_t)row * topk;
   const int steps = (topk + A4_STEP - 1) / A4_STEP;
+  const int first = blockIdx.y * TW_WARPS + warp, stride = gridDim.y * TW_WARPS;
+  uint8_t *ring = a4_smem + warp * TWB_STAGES * TWB_STAGE;
+  // copies: chunk lane % 16 of the tokens 2i + lane / 16
+  const uint8_t *keys = reinterpret_cast<const uint8_t *>(k) + (size_t)kbase * TWB_ROW +
+                        (lane & 15) * 16;
+  const uint32_t dst = smem_u32(ring) + (lane >> 4) * TWB_ROW +
+                       (((lane & 15) ^ ((lane >> 4) << 2)) << 4);
+  auto token = [&](int n) {
+    const int e = n * A4_STEP + lane;
+    return e < topk ? __ldg(irow + e) : -1;
+  };
+  auto copy = [&](int &j, int stage) {  // j: this lane's token, -1 where it is none
+    if (j >= kcap) {
+      raise_status(status, HISA_ERR_INVALID_ARG);
+      j = -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      const int t = __shfl_sync(0xffffffffu, j, 2 * i + (lane >> 4));
+      cp_async_16_or_zero(dst + stage * TWB_STAGE + i * 2 * TWB_ROW,
+                          keys + (size_t)(uint32_t)max(t, 0) * TWB_ROW, t >= 0);
+    }
+    cp_async_commit();
+  };
+  int tok[TWB_STAGES];  // of the steps in flight, oldest first
+#pragma unroll
+  for (int i = 0; i < TWB_STAGES - 1; i++) {
+    tok[i] = token(first + i * stride);
+    copy(tok[i], i);
+  }
+  int next = token(first + (TWB_STAGES - 1) * stride);
   uint4 qw[MT][2][4];
-  float fl[MT][2];
+  float f[MT][2];
+  const float rest = scale_rest(scale);
+  NegLse nl[MT][2];
 #pragma unroll
   for (int mt = 0; mt < MT; mt++)
 #pragma unroll
@@ -745,47 +1139,46 @@ token_weights_kernel(const uint16_t *__restrict__ q, const uint16_t *__restrict_
 #pragma unroll
       for (int i = 0; i < 4; i++)
         qw[mt][r][i] = h < H ? __ldg(reinterpret_cast<const uint4 *>(
-                                         q + ((size_t)row * H + h) * KV4_DIM + 32 * c) + i)
+                                         q + ((size_t)row * H + h) * KV4_DIM) + 4 * i + c)
                              : make_uint4(0u, 0u, 0u, 0u);
-      const float v = h < H ? __ldg(lse + (size_t)row * H + h) : -__int_as_float(0x7f800000);
-      fl[mt][r] = v == -__int_as_float(0x7f800000) ? -v : v * LOG2E;
+      f[mt][r] = scale * LOG2E;
+      nl[mt][r] = neg_lse(lse, (size_t)row, H, h);
     }
-  const float f = scale * LOG2E;
-  for (int n = blockIdx.y * TW_WARPS + warp; n < steps; n += gridDim.y * TW_WARPS) {
-    const int e = n * A4_STEP + lane;
-    int tok = e < topk ? __ldg(irow + e) : -1;
-    if (tok >= kcap) {
-      raise_status(status, HISA_ERR_INVALID_ARG);
-      tok = -1;
-    }
-    if (!__any_sync(0xffffffffu, tok >= 0)) continue;
-    float x[MT][4][4];
+  const uint8_t *place = ring + g * TWB_ROW + ((c ^ ((g & 1) << 2)) << 4);
+  int stage = 0;
+  for (int n = first; n < steps; n += stride) {
+    cp_async_wait_group<TWB_STAGES - 2>();
+    __syncwarp();  // the step has landed for every lane, and the stage before it is read
+    const int now = tok[0];
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const int t = __shfl_sync(0xffffffffu, tok, 8 * j + g);
-      uint4 kw[4];
+    for (int i = 0; i + 2 < TWB_STAGES; i++) tok[i] = tok[i + 1];
+    tok[TWB_STAGES - 2] = next;
+    copy(tok[TWB_STAGES - 2], stage == 0 ? TWB_STAGES - 1 : stage - 1);
+    next = token(n + TWB_STAGES * stride);
+    const uint8_t *at = place + stage * TWB_STAGE;
+    stage = stage == TWB_STAGES - 1 ? 0 : stage + 1;
+    if (!__any_sync(0xffffffffu, now >= 0)) continue;
+    float x[MT][4][4], v[8];
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        kw[i] = t >= 0 ? __ldg(reinterpret_cast<const uint4 *>(
-                                   k + ((size_t)kbase + t) * KV4_DIM + 32 * c) + i)
-                       : make_uint4(0u, 0u, 0u, 0u);
+    for (int j = 0; j < 4; j++)
 #pragma unroll
-      for (int mt = 0; mt < MT; mt++) {
+      for (int i = 0; i < 4; i++) {
+        // chunk 4i + c of an odd token is at (4i + c) ^ 4: the neighbouring pair's place
+        const uint4 kw = *reinterpret_cast<const uint4 *>(
+            at + j * 8 * TWB_ROW + ((i >> 1) << 7) + ((i & 1) ? ((g & 1) ? -64 : 64) : 0));
 #pragma unroll
-        for (int u = 0; u < 4; u++) x[mt][j][u] = 0.f;
+        for (int mt = 0; mt < MT; mt++) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_bf16(d, qw[mt][0][i].x, qw[mt][1][i].x, qw[mt][0][i].y, qw[mt][1][i].y, kw.x, kw.y);
+          mma_bf16(d, qw[mt][0][i].z, qw[mt][1][i].z, qw[mt][0][i].w, qw[mt][1][i].w, kw.z, kw.w);
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          mma_bf16(x[mt][j], qw[mt][0][i].x, qw[mt][1][i].x, qw[mt][0][i].y, qw[mt][1][i].y,
-                   kw[i].x, kw[i].y);
-          mma_bf16(x[mt][j], qw[mt][0][i].z, qw[mt][1][i].z, qw[mt][0][i].w, qw[mt][1][i].w,
-                   kw[i].z, kw[i].w);
+          for (int u = 0; u < 4; u++) x[mt][j][u] = i == 0 ? d[u] : x[mt][j][u] + d[u];
         }
-#pragma unroll
-        for (int u = 0; u < 4; u++) x[mt][j][u] *= f;
       }
-    }
-    add_weights<MT>(x, fl, tok, (size_t)kbase, lane, weights, status);
+    weigh<MT>(x, f, rest, nl, v);
+    add_weights(v, now, weights + kbase, lane, status);
   }
+  cp_async_wait_all();
 }
 
 // CTAs per row: enough to fill the GPU, at most one step per warp
@@ -801,36 +1194,13 @@ cudaError_t launch_token_weights(const uint16_t *q, const uint16_t *k, const int
                                  int num_sms, int *status, cudaStream_t st) {
   const dim3 grid(total_q, weight_splits(total_q, topk, num_sms));
   unsigned long long *w = reinterpret_cast<unsigned long long *>(weights);
-  ProfScope ps(K_TOKEN_WEIGHTS, st);
-  if (H <= 16)
-    token_weights_kernel<1><<<grid, TW_WARPS * 32, 0, st>>>(q, k, idx, lse, cu_q, cu_k, S, H, topk,
-                                                            scale, w, status);
-  else
-    token_weights_kernel<2><<<grid, TW_WARPS * 32, 0, st>>>(q, k, idx, lse, cu_q, cu_k, S, H, topk,
-                                                            scale, w, status);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_token_weights_kv4(const uint16_t *q, const uint8_t *kv4,
-                                     const uint8_t *kv4_scale, const int32_t *idx,
-                                     const float *lse, const int32_t *cu_q, const int32_t *cu_k,
-                                     int S, int total_q, int H, int topk, float scale,
-                                     int64_t *weights, int num_sms, int *status, cudaStream_t st) {
-  const dim3 grid(total_q, weight_splits(total_q, topk, num_sms));
-  unsigned long long *w = reinterpret_cast<unsigned long long *>(weights);
-  constexpr size_t ring = (size_t)TW_WARPS * 3 * A4_STAGE, qb = 2 * 8 * 32 * 16;
+  constexpr size_t smem = (size_t)TW_WARPS * TWB_STAGES * TWB_STAGE;
   static std::atomic<int> attr[2][64];
-  cudaError_t e = H <= 16 ? set_smem_once((const void *)token_weights_kv4_kernel<1>, ring, attr[0])
-                          : set_smem_once((const void *)token_weights_kv4_kernel<2>, ring + qb,
-                                          attr[1]);
+  const auto fn = H <= 16 ? token_weights_kernel<1> : token_weights_kernel<2>;
+  const cudaError_t e = set_smem_once((const void *)fn, smem, attr[H > 16]);
   if (e != cudaSuccess) return e;
   ProfScope ps(K_TOKEN_WEIGHTS, st);
-  if (H <= 16)
-    token_weights_kv4_kernel<1><<<grid, TW_WARPS * 32, ring, st>>>(
-        q, kv4, kv4_scale, idx, lse, cu_q, cu_k, S, H, topk, scale, w, status);
-  else
-    token_weights_kv4_kernel<2><<<grid, TW_WARPS * 32, ring + qb, st>>>(
-        q, kv4, kv4_scale, idx, lse, cu_q, cu_k, S, H, topk, scale, w, status);
+  fn<<<grid, TW_WARPS * 32, smem, st>>>(q, k, idx, lse, cu_q, cu_k, S, H, topk, scale, w, status);
   return cudaGetLastError();
 }
 

@@ -37,8 +37,16 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) {
 // 0x5400 is 64 and its low mantissa bit 1/16, so or-ing the nibble into bits 4..7 gives
 // 64 + u, and (64 + u) * s - 72 * s = (u - 8) * s, rounded once and exact.
 // c72 = -72 * s (72 has 4 significant bits, so it is exact too, and finite: s <= 896).
-__device__ __forceinline__ uint32_t kv4_pair(uint32_t w, __half2 s, __half2 c72) {
-  const uint32_t t = (w & 0x00F000F0u) | 0x54005400u;
+// The magic number comes from a register that the compiler does not see through: of two
+// constants it would make two logic operations.
+__device__ __forceinline__ uint32_t kv4_magic() {
+  uint32_t m;
+  asm("mov.b32 %0, 0x54005400;" : "=r"(m));
+  return m;
+}
+__device__ __forceinline__ uint32_t kv4_pair(uint32_t w, uint32_t magic, __half2 s, __half2 c72) {
+  uint32_t t;  // (w & 0x00F000F0) | magic
+  asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(t) : "r"(w), "r"(magic));
   return as_u32(__hfma2(as_half2(t), s, c72));
 }
 
@@ -58,6 +66,16 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// D = A * B
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1,
+                                              uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -65,6 +83,26 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %5};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 // 2^x (the hardware approximation: relative error about 2^-22, 2^-inf = 0)
