@@ -72,7 +72,7 @@ cudaError_t launch_token_weights(const uint16_t *q, const uint16_t *k, const int
 cudaError_t launch_evict_select(const int64_t *weights, const int32_t *cu_k,
                                 const int32_t *seqlens, const int32_t *keep, int S,
                                 int max_seqlen_k, int n_sink, int n_recent, int32_t *kept,
-                                int32_t *kept_len, int *status, cudaStream_t st);
+                                int32_t *kept_len, int num_sms, int *status, cudaStream_t st);
 cudaError_t launch_evict_rows(const hisa_rows *arrays, int n, const int32_t *cu_src,
                               const int32_t *cu_dst, const int32_t *kept, const int32_t *kept_len,
                               int S, int max_keep, int num_sms, int *status, cudaStream_t st);
@@ -611,7 +611,7 @@ hisa_status hisa_evict_select(const int64_t *weights, const int32_t *cu_seqlens_
   int *st = status_word();
   if (!st) return HISA_ERR_CUDA;
   return from_cuda(launch_evict_select(weights, cu_seqlens_k, seqlens_k, keep, num_seqs,
-                                       max_seqlen_k, n_sink, n_recent, kept, kept_len, st,
+                                       max_seqlen_k, n_sink, n_recent, kept, kept_len, num_sms(), st,
                                        static_cast<cudaStream_t>(stream)));
 }
 
