@@ -56,10 +56,12 @@ cudaError_t launch_decode_select(const uint16_t *q, const uint16_t *k, const flo
                                  const uint16_t *new_keys = nullptr);
 cudaError_t launch_kv4_store(const uint16_t *k_new, const uint16_t *v_new, const int32_t *cu_q,
                              const int32_t *cu_k, const int32_t *seqlens, int S, int total_q,
-                             uint8_t *kv4, uint8_t *kv4_scale, int *status, cudaStream_t st);
+                             uint8_t *kv4, uint8_t *kv4_scale, int num_sms, int *status,
+                             cudaStream_t st);
 cudaError_t launch_kv4_load(const uint8_t *kv4, const uint8_t *kv4_scale, const int32_t *cu_q,
                             const int32_t *cu_k, const int32_t *seqlens, int S, int total_q,
-                            uint16_t *k_out, uint16_t *v_out, int *status, cudaStream_t st);
+                            uint16_t *k_out, uint16_t *v_out, int num_sms, int *status,
+                            cudaStream_t st);
 cudaError_t launch_attention_kv4(const uint16_t *q, const uint8_t *kv4, const uint8_t *kv4_scale,
                                  const int32_t *idx, const int32_t *cu_q, const int32_t *cu_k,
                                  int S, int total_q, int H, int topk, float scale, uint16_t *out,
@@ -527,7 +529,7 @@ hisa_status hisa_kv4_store(const hisa_bf16 *k_new, const hisa_bf16 *v_new,
   int *st = status_word();
   if (!st) return HISA_ERR_CUDA;
   return from_cuda(launch_kv4_store(k_new, v_new, cu_seqlens_q, cu_seqlens_k, seqlens_k, num_seqs,
-                                    total_q, kv4, kv4_scale, st,
+                                    total_q, kv4, kv4_scale, num_sms(), st,
                                     static_cast<cudaStream_t>(stream)));
 }
 
@@ -546,7 +548,7 @@ hisa_status hisa_kv4_load(const uint8_t *kv4, const uint8_t *kv4_scale,
   int *st = status_word();
   if (!st) return HISA_ERR_CUDA;
   return from_cuda(launch_kv4_load(kv4, kv4_scale, cu_seqlens_q, cu_seqlens_k, seqlens_k,
-                                   num_seqs, total_q, k_out, v_out, st,
+                                   num_seqs, total_q, k_out, v_out, num_sms(), st,
                                    static_cast<cudaStream_t>(stream)));
 }
 

@@ -42,13 +42,12 @@ constexpr int A4_STEP = 32;                                   // tokens of a war
 constexpr int A4_CODES = A4_STEP * KV4_ROW;                   // 4096 bytes
 constexpr int A4_STAGE = A4_CODES + A4_STEP * KV4_NS;         // 4608
 constexpr int A4_MAX_CLUSTER = 8;
-constexpr int A4_SCORE_TOKENS = 512;  // tokens of a CTA that keeps its scores for the weights
 constexpr float A4_TAU = 8.f;    // tolerated growth of a head's maximum, in powers of two
 constexpr int A4_OSTRIDE = KV4_DIM + 4;                       // padded row of partial outputs
 constexpr float LOG2E = 1.4426950408889634f, LOG2E_LO = 1.92596303e-8f, LN2 = 0.6931471805599453f;
 
 constexpr int A4_WARPS = 4, A4_THREADS = A4_WARPS * 32;
-__host__ __device__ constexpr int a4_stages(int MT) { return MT == 1 ? 3 : 4; }
+__host__ __device__ constexpr int a4_stages(int MT) { return MT == 1 ? 2 : 4; }
 // CTAs of an SM: one or two 16-head tiles in up to 168 or 255 registers per thread
 __host__ __device__ constexpr int a4_ctas(int MT) { return MT == 1 ? 3 : 2; }
 // a warp's ring, which later holds its partial output
@@ -68,6 +67,18 @@ __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *sr
                "r"(ok ? 16 : 0)
                : "memory");
 }
+// the warp's number, told to the compiler as one that all its lanes share
+__device__ __forceinline__ int warp_index() {
+  return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+}
+
+// A load from shared memory by its 32-bit address: the walks below keep such addresses, at
+// half the registers of pointers.
+template <typename T>
+__device__ __forceinline__ T lds(uint32_t at) {
+  return *reinterpret_cast<const T *>(__cvta_shared_to_generic(at));
+}
+
 // p + j * KV4_ROW in one multiply-add
 __device__ __forceinline__ const uint8_t *row_of(const uint8_t *p, int j) {
   uint64_t r;
@@ -155,7 +166,7 @@ __device__ __forceinline__ void load_query(const uint16_t *__restrict__ q, size_
 struct LanePlaces {
   uint32_t kc, ks;        // token g: the lane's 16 key bytes, its two key scales
   uint32_t v0, v1;        // tokens 2c and 2c + 1: the lane's 8 value bytes
-  uint32_t s0, s1;        // and their value scales
+  uint32_t s0;            // token 2c: its value scale
   uint32_t d0, d1;        // copies: chunks lane % 4 and lane % 4 + 4 of token lane / 4
   __device__ __forceinline__ explicit LanePlaces(int lane) {
     const int g = lane >> 2, c = lane & 3, t = 2 * c;
@@ -164,20 +175,19 @@ struct LanePlaces {
     v0 = t * KV4_ROW + (a4_chunk(t, 4 + (g >> 1)) << 4) + (g & 1) * 8;
     v1 = (t + 1) * KV4_ROW + (a4_chunk(t + 1, 4 + (g >> 1)) << 4) + (g & 1) * 8;
     s0 = A4_CODES + t * KV4_NS + 8 + g;
-    s1 = s0 + KV4_NS;
     d0 = g * KV4_ROW + (a4_chunk(g, c) << 4);
     d1 = g * KV4_ROW + (a4_chunk(g, c + 4) << 4);
   }
 };
 
 // Raw scores of the tokens 8j .. 8j + 7 of a ring stage: s[mt] is their score fragment.
-// qs: the query fragments at this lane's place.
+// qs: the query fragments at this lane's place (shared address).
 template <int MT>
-__device__ __forceinline__ void kv4_scores(const uint8_t *stage, int j, const LanePlaces &lp,
-                                           const uint4 *qs, uint32_t magic,
+__device__ __forceinline__ void kv4_scores(uint32_t stage, int j, const LanePlaces &lp,
+                                           uint32_t qs, uint32_t magic,
                                            float (&s)[MT][4][4]) {
-  const uint4 kw = *reinterpret_cast<const uint4 *>(stage + lp.kc + j * 8 * KV4_ROW);
-  const uint32_t sb = *reinterpret_cast<const uint16_t *>(stage + lp.ks + j * 8 * KV4_NS);
+  const uint4 kw = lds<uint4>(stage + lp.kc + j * 8 * KV4_ROW);
+  const uint32_t sb = lds<uint16_t>(stage + lp.ks + j * 8 * KV4_NS);
   const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -189,7 +199,8 @@ __device__ __forceinline__ void kv4_scores(const uint8_t *stage, int j, const La
     const uint32_t b3 = kv4_pair(w[i] >> 8, magic, sc, c72);
 #pragma unroll
     for (int mt = 0; mt < MT; mt++) {
-      const uint4 qa = qs[(mt * 8 + 2 * i) * 32], qb = qs[(mt * 8 + 2 * i + 1) * 32];
+      const uint4 qa = lds<uint4>(qs + (mt * 8 + 2 * i) * 512);
+      const uint4 qb = lds<uint4>(qs + (mt * 8 + 2 * i + 1) * 512);
       if (i == 0)
         mma_f16_first(s[mt][j], qa.x, qa.y, qa.z, qa.w, b0, b1);
       else
@@ -203,13 +214,13 @@ __device__ __forceinline__ void kv4_scores(const uint8_t *stage, int j, const La
 struct ValueRaw {
   uint2 v[4];              // nibbles of the tokens 2c, 2c + 1, 2c + 8, 2c + 9
   __half2 s0, s1, k0, k1;  // their scales in pairs, and -72 times them
-  __device__ __forceinline__ void load(const uint8_t *stage, int i, const LanePlaces &lp) {
+  __device__ __forceinline__ void load(uint32_t stage, int i, const LanePlaces &lp) {
     uint32_t sb[4];
 #pragma unroll
     for (int u = 0; u < 4; u++) {
       const int t = 16 * i + 8 * (u >> 1);
-      v[u] = *reinterpret_cast<const uint2 *>(stage + ((u & 1) ? lp.v1 : lp.v0) + t * KV4_ROW);
-      sb[u] = stage[((u & 1) ? lp.s1 : lp.s0) + t * KV4_NS];
+      v[u] = lds<uint2>(stage + ((u & 1) ? lp.v1 : lp.v0) + t * KV4_ROW);
+      sb[u] = lds<uint8_t>(stage + lp.s0 + (t + (u & 1)) * KV4_NS);
     }
     s0 = as_half2(__byte_perm(sb[0], sb[1], 0x5410) << 7);
     s1 = as_half2(__byte_perm(sb[2], sb[3], 0x5410) << 7);
@@ -253,8 +264,7 @@ struct Ring {
   int first_e;                      // and of the first
   int kcap;
   const uint8_t *codes, *scales;    // the region's first row; codes at this lane's chunk
-  uint8_t *ring;
-  uint32_t slot, fill;              // bytes to the stage of the next step, and of the next copy
+  uint32_t ring, slot, fill;        // shared address; bytes to the stage of the next step, and copy
   int next_tok;                     // this lane's token of the next step to copy (-1 = none)
   uint32_t mask[AHEAD];             // valid tokens of the steps in flight, oldest first
   bool bad;
@@ -272,7 +282,7 @@ struct Ring {
     kcap = cap;
     codes = kv4 + (size_t)kbase * KV4_ROW + (lane & 3) * 16;
     scales = kv4_scale + (size_t)kbase * KV4_NS;
-    ring = mem;
+    ring = smem_u32(mem);
     slot = fill = 0;
     bad = false;
     read();
@@ -293,7 +303,7 @@ struct Ring {
       j = -1;
     }
     const uint32_t valid = __ballot_sync(0xffffffffu, j >= 0);
-    const uint32_t dst = smem_u32(ring) + fill;
+    const uint32_t dst = ring + fill;
     fill = after(fill);
     const uint32_t a0 = dst + lp.d0, a1 = dst + lp.d1;
     // four lanes copy 64 bytes of a token together, eight tokens at a time
@@ -324,7 +334,7 @@ struct Ring {
     for (int n = 0; n < AHEAD; n++) mask[n] = copy(lp, lane);
   }
   // start one more copy, wait for the next step; its stage and the mask of its valid tokens
-  __device__ __forceinline__ const uint8_t *arrive(const LanePlaces &lp, int lane,
+  __device__ __forceinline__ uint32_t arrive(const LanePlaces &lp, int lane,
                                                    uint32_t &valid) {
     __syncwarp();  // every lane has read the stage that is filled now
     const uint32_t more = copy(lp, lane);
@@ -334,7 +344,7 @@ struct Ring {
     mask[AHEAD - 1] = more;
     cp_async_wait_group<AHEAD>();
     __syncwarp();  // the step has landed for every lane
-    const uint8_t *stage = ring + slot;
+    const uint32_t stage = ring + slot;
     slot = after(slot);
     return stage;
   }
@@ -434,12 +444,10 @@ struct Running {
   }
 };
 
-// All steps of a warp's ring.  KEEP: the raw scores go to `scores` (this lane's place), one
-// step's after another's `step_scores` further on.
-template <int MT, bool KEEP, typename R>
-__device__ __forceinline__ void attend(R &ring, const LanePlaces &lp, const uint4 *qf,
-                                       const float (&f)[MT][2], int lane, Running<MT> &st,
-                                       float4 *scores, int step_scores) {
+// All steps of a warp's ring.
+template <int MT, typename R>
+__device__ __forceinline__ void attend(R &ring, const LanePlaces &lp, uint32_t qf,
+                                       const float (&f)[MT][2], int lane, Running<MT> &st) {
   const float NEG = -__int_as_float(0x7f800000);
   const int c = lane & 3;
   const uint32_t magic = kv4_magic();
@@ -448,19 +456,11 @@ __device__ __forceinline__ void attend(R &ring, const LanePlaces &lp, const uint
   auto &l = st.l;
   for (int n = 0; n < ring.nsteps; n++) {
     uint32_t valid;
-    const uint8_t *stage = ring.arrive(lp, lane, valid);
+    const uint32_t stage = ring.arrive(lp, lane, valid);
     if (!valid) continue;
     float x[MT][4][4];
 #pragma unroll
     for (int j = 0; j < 4; j++) kv4_scores(stage, j, lp, qf, magic, x);
-    if (KEEP) {
-#pragma unroll
-      for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-          scores[(size_t)n * step_scores + (mt * 4 + j) * 32] =
-              make_float4(x[mt][j][0], x[mt][j][1], x[mt][j][2], x[mt][j][3]);
-    }
     // exponents against the reference maxima; -inf where there is no token
     float top = NEG;
     float y[MT][4][4];
@@ -571,7 +571,7 @@ __device__ __forceinline__ void weigh_step(int mt, int j, const float4 &t, const
 // The weights of a warp's tokens from a second look at their keys; m, inv: the row's
 // maxima and inverse sums.
 template <int MT, typename R>
-__device__ __forceinline__ void weigh_again(R &ring, const LanePlaces &lp, const uint4 *qf,
+__device__ __forceinline__ void weigh_again(R &ring, const LanePlaces &lp, uint32_t qf,
                                             const float (&f)[MT][2], const float (&m)[MT][2],
                                             const float (&inv)[MT][2], int lane,
                                             unsigned long long *weights, int *status) {
@@ -580,7 +580,7 @@ __device__ __forceinline__ void weigh_again(R &ring, const LanePlaces &lp, const
   const int32_t *entry = ring.irow + ring.first_e;
   for (int n = 0; n < ring.nsteps; n++) {
     uint32_t valid;
-    const uint8_t *stage = ring.arrive(lp, lane, valid);
+    const uint32_t stage = ring.arrive(lp, lane, valid);
     if (!valid) continue;
     const int tok = (valid >> lane) & 1u ? __ldg(entry + (size_t)n * ring.stride) : -1;
     float x[MT][4][4], v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -648,29 +648,12 @@ __device__ __forceinline__ float lse_of(float mx, float sum) {
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: W = 1 or 2 warps per row, so that a row's start and end (about 3000 cycles of
-// latency) hide behind the other warps of the SM and, for one warp, nothing is merged.
+// Many rows: a row is one warp's, so that its start and end (about 3000 cycles of latency)
+// hide behind the other warps of the SM and nothing is merged.
 
-template <int MT>
-constexpr size_t rows_smem(int W) {
-  return (size_t)A4_WARPS * a4_ring(MT) + (size_t)(A4_WARPS / W) * MT * 4096 +
-         (size_t)A4_WARPS * 16 * MT * 8;
-}
-
-template <int ID, int N>
-__device__ __forceinline__ void asm_bar() {
-  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory");
-}
-template <int W>
-__device__ __forceinline__ void sync_row(int group) {
-  static_assert(W <= 2, "two rows of two warps");
-  if (W == 1)
-    __syncwarp();
-  else
-    group ? asm_bar<2, W * 32>() : asm_bar<1, W * 32>();
-}
-
-template <int MT, int W, bool WT>
+// WT: with weights (a kernel of its own: what the second look needs would cost the first
+// one registers, 561 us against 639 for 8192 rows of 2048 tokens and 16 heads).
+template <int MT, bool WT>
 __global__ void __launch_bounds__(A4_THREADS, a4_ctas(MT))
 attn_kv4_rows_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict__ kv4,
                      const uint8_t *__restrict__ kv4_scale, const int32_t *__restrict__ idx,
@@ -679,112 +662,60 @@ attn_kv4_rows_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict__
                      float *__restrict__ lse, unsigned long long *__restrict__ weights,
                      int *status) {
   extern __shared__ __align__(16) uint8_t a4_smem[];
-  constexpr int NST = a4_stages(MT), RING = a4_ring(MT), NH = 16 * MT;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int group = warp / W, part = warp % W;
-  const int row = blockIdx.x * (A4_WARPS / W) + group;
-  if (row >= total_q) return;  // all of the row's warps
+  constexpr int NST = a4_stages(MT), RING = a4_ring(MT);
+  const int lane = threadIdx.x & 31, warp = warp_index();
+  const int row = blockIdx.x * A4_WARPS + warp;
+  if (row >= total_q) return;  // the whole warp; the others do not wait for it
   const int g = lane >> 2, c = lane & 3;
-  uint4 *qs = reinterpret_cast<uint4 *>(a4_smem + A4_WARPS * RING + group * MT * 4096);
-  float *wm = reinterpret_cast<float *>(a4_smem + A4_WARPS * RING +
-                                        (A4_WARPS / W) * MT * 4096) + group * 2 * W * NH;
-  float *wl = wm + W * NH;
+  uint4 *qs = reinterpret_cast<uint4 *>(a4_smem + A4_WARPS * RING + warp * MT * 4096);
   uint8_t *mem = a4_smem + warp * RING;
 
-  const int s = find_seq(cu_q, S, row);
+  const int s = find_seq_warp(cu_q, S, row, lane);
   const int kbase = __ldg(cu_k + s), kcap = __ldg(cu_k + s + 1) - kbase;
   const LanePlaces lp(lane);
   const int32_t *irow = idx + (size_t)row * topk;
   Ring<NST, NST - 1, true> ring;
-  ring.init(irow, 0, topk, part, W, kbase, kcap, kv4, kv4_scale, mem, lane);
+  ring.init(irow, 0, topk, 0, 1, kbase, kcap, kv4, kv4_scale, mem, lane);
   ring.start(lp, lane);
   float f[MT][2];
-  load_query<MT, W>(q, (size_t)row, H, scale, qs, lane, part, f);
-  sync_row<W>(group);
-  const uint4 *qf = qs + lane;
+  load_query<MT, 1>(q, (size_t)row, H, scale, qs, lane, 0, f);
+  __syncwarp();
+  const uint32_t qf = smem_u32(qs + lane);
   Running<MT> st;
   st.clear();
-  attend<MT, false>(ring, lp, qf, f, lane, st, nullptr, 0);
+  attend<MT>(ring, lp, qf, f, lane, st);
   if (__any_sync(0xffffffffu, ring.bad) && lane == 0) raise_status(status, HISA_ERR_INVALID_ARG);
 
-  float mx[MT][2], inv[MT][2];  // of the row (W = 1), for the outputs and the weights
-  if (W == 1) {
+  float mx[MT][2], inv[MT][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; mt++)
+  for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-      for (int r = 0; r < 2; r++) {
-        const int h = 16 * mt + g + 8 * r;
-        const float sum = st.total(mt, r);
-        mx[mt][r] = st.m[mt][r];
-        inv[mt][r] = inverse_sum(sum);
-        if (h >= H) continue;
-        if (c == 0 && lse) lse[(size_t)row * H + h] = lse_of(mx[mt][r], sum);
-        // the lane's 32 dimensions: 16 of column 2c, 16 of column 2c + 1
-        uint4 *dst = reinterpret_cast<uint4 *>(out + ((size_t)row * H + h) * KV4_DIM + 32 * c);
+    for (int r = 0; r < 2; r++) {
+      const int h = 16 * mt + g + 8 * r;
+      const float sum = st.total(mt, r);
+      mx[mt][r] = st.m[mt][r];
+      inv[mt][r] = inverse_sum(sum);
+      if (h >= H) continue;
+      if (c == 0 && lse) lse[(size_t)row * H + h] = lse_of(mx[mt][r], sum);
+      // the lane's 32 dimensions: 16 of column 2c, 16 of column 2c + 1
+      uint4 *dst = reinterpret_cast<uint4 *>(out + ((size_t)row * H + h) * KV4_DIM + 32 * c);
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-          uint32_t w[4];
+      for (int u = 0; u < 4; u++) {
+        uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const int t = 8 * (u & 1) + 2 * i, e = 2 * r + (u >> 1);
-            const __nv_bfloat162 b = __floats2bfloat162_rn(st.o[mt][t][e] * inv[mt][r],
-                                                           st.o[mt][t + 1][e] * inv[mt][r]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&b);
-          }
-          dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 4; i++) {
+          const int t = 8 * (u & 1) + 2 * i, e = 2 * r + (u >> 1);
+          const __nv_bfloat162 b = __floats2bfloat162_rn(st.o[mt][t][e] * inv[mt][r],
+                                                         st.o[mt][t + 1][e] * inv[mt][r]);
+          w[i] = *reinterpret_cast<const uint32_t *>(&b);
         }
+        dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-  } else {
-    store_share<MT>(st, mem, wm + part * NH, wl + part * NH, lane);
-    sync_row<W>(group);
-    // every thread of the row finishes some pieces; the factors it needs it works out
-    // itself, and the row's maxima and inverse sums of its fragments' heads
-    const uint8_t *shares = a4_smem + group * W * RING;
-    for (int x = part * 32 + lane; x < H * (KV4_DIM / 4); x += W * 32) {
-      const int h = x >> 5, b = (x >> 3) & 3, u = x & 7;
-      float top = -__int_as_float(0x7f800000), sum = 0.f, a[W];
-#pragma unroll
-      for (int w = 0; w < W; w++) top = fmaxf(top, wm[w * NH + h]);
-#pragma unroll
-      for (int w = 0; w < W; w++) {
-        const float lw = wl[w * NH + h];
-        a[w] = share_factor(wm[w * NH + h], lw, top);
-        sum += lw != lw ? lw : a[w] * lw;
-      }
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < W; w++)
-        add_share(acc, a[w],
-                  *reinterpret_cast<const float4 *>(
-                      reinterpret_cast<const float *>(shares + w * RING) + h * A4_OSTRIDE +
-                      32 * b + 4 * (u ^ (2 * b))));
-      store_out(out + ((size_t)row * H + h) * KV4_DIM + 32 * b + 4 * u, acc, inverse_sum(sum));
-      if (lse && (x & 31) == 0) lse[(size_t)row * H + h] = lse_of(top, sum);
     }
-    if (WT) {
-#pragma unroll
-      for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-        for (int r = 0; r < 2; r++) {
-          const int h = 16 * mt + g + 8 * r;
-          float top = -__int_as_float(0x7f800000), sum = 0.f;
-#pragma unroll
-          for (int w = 0; w < W; w++) top = fmaxf(top, wm[w * NH + h]);
-#pragma unroll
-          for (int w = 0; w < W; w++) {
-            const float lw = wl[w * NH + h];
-            sum += lw != lw ? lw : share_factor(wm[w * NH + h], lw, top) * lw;
-          }
-          mx[mt][r] = top;
-          inv[mt][r] = inverse_sum(sum);
-        }
-      sync_row<W>(group);  // the shares are read: the rings take keys again
-    }
-  }
   if (WT) {
     dead_heads<MT>(H, g, f, mx, inv);
     Ring<NST, NST - 1, false> again;
-    again.init(irow, 0, topk, part, W, kbase, kcap, kv4, kv4_scale, mem, lane);
+    again.init(irow, 0, topk, 0, 1, kbase, kcap, kv4, kv4_scale, mem, lane);
     weigh_again<MT>(again, lp, qf, f, mx, inv, lane, weights + kbase, status);
   }
 }
@@ -797,11 +728,10 @@ struct SplitSmem {
   static constexpr int QBYTES = MT * 4096;
   static constexpr int NH = 16 * MT;
   // ring of every warp | query fragments | m, l of every warp and head | m, l of the CTA |
-  // merge factors of the cluster | scores (weights only, one step's 32 tokens after another)
+  // merge factors of the cluster
   static constexpr size_t bytes = (size_t)A4_WARPS * a4_ring(MT) + QBYTES +
                                   (size_t)A4_WARPS * NH * 8 + (size_t)NH * 8 +
                                   (size_t)NH * A4_MAX_CLUSTER * 4;
-  static constexpr size_t STEP_SCORES = (size_t)A4_STEP * NH * 4;
 };
 
 template <int MT, bool WT>
@@ -825,11 +755,7 @@ attn_kv4_split_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict_
   float *wl = wm + A4_WARPS * NH;                                     // [warps][NH]
   float *cm = wl + A4_WARPS * NH, *cs = cm + NH;  // the CTA's maximum and sum per head
   float *xm = cs + NH;                            // factors of the cluster's CTAs [NH][C]
-  // scores of this warp's steps: the lane that wrote a value reads it back
-  constexpr int STEP = (int)(SplitSmem<MT>::STEP_SCORES / 16);
-  float4 *scores = reinterpret_cast<float4 *>(xm + NH * A4_MAX_CLUSTER) + warp * STEP + lane;
-
-  const int s = find_seq(cu_q, S, row);
+  const int s = find_seq_warp(cu_q, S, row, lane);
   const int kbase = __ldg(cu_k + s), kcap = __ldg(cu_k + s + 1) - kbase;
   const LanePlaces lp(lane);
   const int e0 = me * per_cta, e1 = min(topk, e0 + per_cta);
@@ -841,10 +767,10 @@ attn_kv4_split_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict_
   float f[MT][2];
   load_query<MT, A4_WARPS>(q, (size_t)row, H, scale, reinterpret_cast<uint4 *>(qs), lane, warp, f);
   __syncthreads();
-  const uint4 *qf = reinterpret_cast<const uint4 *>(qs) + lane;
+  const uint32_t qf = smem_u32(qs + lane * 16);
   Running<MT> st;
   st.clear();
-  attend<MT, WT>(ring, lp, qf, f, lane, st, scores, A4_WARPS * STEP);
+  attend<MT>(ring, lp, qf, f, lane, st);
   if (__any_sync(0xffffffffu, ring.bad) && lane == 0) raise_status(status, HISA_ERR_INVALID_ARG);
   store_share<MT>(st, mem, wm + warp * NH, wl + warp * NH, lane);
   __syncthreads();
@@ -913,7 +839,6 @@ attn_kv4_split_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict_
       __syncthreads();
     }
   }
-  // The weights: the scores are there, the row's maxima and sums known.
   if (WT) {
     float mx[MT][2], inv[MT][2];
 #pragma unroll
@@ -924,20 +849,15 @@ attn_kv4_split_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict_
         inv[mt][r] = wl[16 * mt + g + 8 * r];
       }
     dead_heads<MT>(H, g, f, mx, inv);
-    for (int n = 0; n < ring.nsteps; n++) {
-      const int e = e0 + (warp + n * A4_WARPS) * A4_STEP + lane;
-      int tok = e < e1 ? __ldg(irow + e) : -1;
-      if (tok >= kcap) tok = -1;
-      if (!__any_sync(0xffffffffu, tok >= 0)) continue;
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-          weigh_step<MT>(mt, j, scores[(size_t)n * A4_WARPS * STEP + (mt * 4 + j) * 32], f, mx, inv,
-                         v);
-      add_weights(v, tok, weights + kbase, lane, status);
-    }
+    // the partial outputs in the rings have been read, by this CTA and by the others
+    if (C > 1)
+      cl.sync();
+    else
+      __syncthreads();
+    Ring<NST, NST - 1, false> again;
+    again.init(irow, e0, e1, warp, A4_WARPS, kbase, kcap, kv4, kv4_scale, mem, lane);
+    weigh_again<MT>(again, lp, qf, f, mx, inv, lane, weights + kbase, status);
+    return;
   }
   if (C > 1) cl.sync();  // no CTA leaves while another reads its shared memory
 }
@@ -954,17 +874,16 @@ struct AttnArgs {
   int *status;
 };
 
-template <int MT, int W, bool WT>
+template <int MT, bool WT>
 static cudaError_t launch_rows(const AttnArgs &a, cudaStream_t st) {
   static std::atomic<int> attr[64];
-  constexpr size_t smem = rows_smem<MT>(W);
+  constexpr size_t smem = (size_t)A4_WARPS * (a4_ring(MT) + MT * 4096);
   static_assert((smem + 1024) * a4_ctas(MT) <= 233472, "the CTAs of an SM");
-  const auto fn = attn_kv4_rows_kernel<MT, W, WT>;
+  const auto fn = attn_kv4_rows_kernel<MT, WT>;
   const cudaError_t e = set_smem_once((const void *)fn, smem, attr);
   if (e != cudaSuccess) return e;
-  constexpr int per = A4_WARPS / W;
   ProfScope ps(K_ATTENTION_KV4, st);
-  fn<<<(a.total_q + per - 1) / per, A4_THREADS, smem, st>>>(
+  fn<<<(a.total_q + A4_WARPS - 1) / A4_WARPS, A4_THREADS, smem, st>>>(
       a.q, a.kv4, a.kv4_scale, a.idx, a.cu_q, a.cu_k, a.S, a.total_q, a.H, a.topk, a.scale, a.out,
       a.lse, a.weights, a.status);
   return cudaGetLastError();
@@ -974,12 +893,10 @@ template <int MT, bool WT>
 static cudaError_t launch_split(const AttnArgs &a, int C, cudaStream_t st) {
   static std::atomic<int> attr[64];
   const int per = ((a.topk + A4_STEP - 1) / A4_STEP + C - 1) / C;
-  const size_t smem = SplitSmem<MT>::bytes + (WT ? per * SplitSmem<MT>::STEP_SCORES : 0);
-  constexpr size_t most =
-      SplitSmem<MT>::bytes + (WT ? A4_SCORE_TOKENS / A4_STEP * SplitSmem<MT>::STEP_SCORES : 0);
-  static_assert(most <= 232448, "a CTA's shared memory");
+  constexpr size_t smem = SplitSmem<MT>::bytes;
+  static_assert((smem + 1024) * a4_ctas(MT) <= 233472, "the CTAs of an SM");
   const auto fn = attn_kv4_split_kernel<MT, WT>;
-  const cudaError_t e = set_smem_once((const void *)fn, most, attr);
+  const cudaError_t e = set_smem_once((const void *)fn, smem, attr);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.total_q * C);
@@ -1002,19 +919,23 @@ template <int MT, bool WT>
 static cudaError_t launch_attn(const AttnArgs &a, int num_sms, cudaStream_t st) {
   const int steps = (a.topk + A4_STEP - 1) / A4_STEP;
   // Few rows: a row is split over a CTA's warps, and over the CTAs of a cluster while that
-  // leaves SMs idle and every CTA has a step for each of its warps.
+  // leaves SMs idle and every CTA has a step for each of its warps; up to two CTAs per SM
+  // where it saves at least two steps of each warp (64 rows of 2048 tokens and 16 heads 17.3
+  // us with 2 CTAs, 15.1 with 4; but 128 rows of 256 tokens 8.2 with 1, 10.3 with 2).
   int C = 1;
-  while (C < A4_MAX_CLUSTER && a.total_q * C * 2 <= num_sms && steps >= C * 2 * A4_WARPS) C *= 2;
-  const bool kept = !WT || (steps + C - 1) / C * A4_STEP <= A4_SCORE_TOKENS;
-  // Estimated time in steps of a warp, with a start and end that cost about three: the rows
-  // spread over all warps, and half a row for the last wave's idle warps.
-  const int slots = num_sms * a4_ctas(MT) * A4_WARPS;
-  auto cost = [&](int W) {
-    const double row = (steps + W - 1) / W + 3.0;
-    return (double)a.total_q * W / slots * row + 0.5 * row;
-  };
-  if (kept && (C > 1 || (cost(4) < cost(2) && cost(4) < cost(1)))) return launch_split<MT, WT>(a, C, st);
-  return cost(2) < cost(1) ? launch_rows<MT, 2, WT>(a, st) : launch_rows<MT, 1, WT>(a, st);
+  while (C < A4_MAX_CLUSTER &&
+         ((a.total_q * C * 2 <= num_sms && steps >= C * 2 * A4_WARPS) ||
+          (a.total_q * C <= num_sms && steps >= C * 4 * A4_WARPS)))
+    C *= 2;
+  // With many rows a warp has one to itself.  A row's start and end cost a warp about 2.5
+  // steps, four times if four warps share it; one warp alone leaves half a row's steps idle
+  // in the last wave instead of half of a quarter.  Measured (us, one warp / four): 16 heads,
+  // 2048 tokens 2400 rows 211 / 186, 8192 rows 561 / 591; 512 tokens 1200 rows 38 / 37,
+  // 2400 rows 61 / 65; two warps were never the best of the three by 5%.
+  const long long slots = (long long)num_sms * a4_ctas(MT) * A4_WARPS;
+  const int spared = steps - (steps + A4_WARPS - 1) / A4_WARPS;
+  if (C > 1 || 15ll * a.total_q <= slots * spared) return launch_split<MT, WT>(a, C, st);
+  return launch_rows<MT, WT>(a, st);
 }
 
 cudaError_t launch_attention_kv4(const uint16_t *q, const uint8_t *kv4, const uint8_t *kv4_scale,
@@ -1052,85 +973,93 @@ __device__ __forceinline__ NegLse neg_lse(const float *lse, size_t row, int H, i
   return n;
 }
 
-// What scale * log2(e) loses as one fp32 number, relative to it.
-__device__ __forceinline__ float scale_rest(float scale) {
-  const float hi = scale * LOG2E;
-  return hi == 0.f ? 0.f : (fmaf(scale, LOG2E, -hi) + scale * LOG2E_LO) / hi;
-}
-
-// v[i] = sum over the lane's heads of 2^(x f - lse), x the score fragments of 32 tokens;
-// rest = scale_rest
+// v[i] = sum over the lane's heads of 2^(x f - lse), x the score fragments of 32 tokens, f2
+// what f lost
 template <int MT>
-__device__ __forceinline__ void weigh(const float (&x)[MT][4][4], const float (&f)[MT][2],
-                                      float rest, const NegLse (&nl)[MT][2], float (&v)[8]) {
+__device__ __forceinline__ void weigh(const float (&x)[MT][4][4], float f, float f2,
+                                      const NegLse (&nl)[MT][2], float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    v[i] = 0.f;
+  for (int j = 0; j < 4; j++) {
+    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int mt = 0; mt < MT; mt++)
 #pragma unroll
       for (int r = 0; r < 2; r++) {
-        const float t = x[mt][i >> 1][2 * r + (i & 1)];
-        v[i] += ex2(fmaf(t, f[mt][r], nl[mt][r].hi) + fmaf(t, f[mt][r] * rest, nl[mt][r].lo));
+        const float2 t = make_float2(x[mt][j][2 * r], x[mt][j][2 * r + 1]);
+        const float2 e = add2(fma2(t, f, nl[mt][r].hi), fma2(t, f2, nl[mt][r].lo));
+        sum = add2(sum, make_float2(ex2(e.x), ex2(e.y)));
       }
+    v[2 * j] = sum.x;
+    v[2 * j + 1] = sum.y;
   }
 }
 
-// The rows (256 bytes) come through a ring as above: lane (g, c) takes the 16-byte chunks 4i + c of token g of every 8, chunk i being the fragments 2i
-// and 2i + 1, of the query alike.  The matrix unit cuts sums off instead of rounding them,
-// which in a chain of eight would lower every score by a few 2^-24 of itself and every
-// weight by that times the score; so pairs are summed there and the four sums here.
-constexpr int TWB_STAGES = 3, TWB_ROW = KV4_DIM * 2, TWB_STAGE = A4_STEP * TWB_ROW;
+// The rows (256 bytes) come through a ring as above: lane (g, c) takes the 16-byte chunks
+// 4i + c of token g of every 8, chunk i being the fragments 2i and 2i + 1, of the query
+// alike; an odd token's chunks change places in pairs of four, so that two tokens' fall
+// into different banks.  The matrix unit cuts sums off instead of rounding them, which in a
+// chain of eight would lower every score by a few 2^-24 of itself and every weight by that
+// times the score; so pairs are summed there and the four sums here.
+//
+// A warp has a row, or a part of one, to itself: its start hides behind the other warps.
+constexpr int TWB_ROW = KV4_DIM * 2, TWB_STAGE = A4_STEP * TWB_ROW;
+constexpr int tw_ctas(int MT) { return MT == 1 ? 3 : 2; }  // 168 and 255 registers
+constexpr int tw_smem() { return TW_WARPS * 2 * TWB_STAGE; }
 
 template <int MT>
-__global__ void __launch_bounds__(TW_WARPS * 32, 2)
+__global__ void __launch_bounds__(TW_WARPS * 32, tw_ctas(MT))
 token_weights_kernel(const uint16_t *__restrict__ q, const uint16_t *__restrict__ k,
                      const int32_t *__restrict__ idx, const float *__restrict__ lse,
                      const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, int S,
-                     int H, int topk, float scale, unsigned long long *__restrict__ weights,
-                     int *status) {
+                     int total_q, int parts, int H, int topk, float scale,
+                     unsigned long long *__restrict__ weights, int *status) {
   extern __shared__ __align__(16) uint8_t a4_smem[];
-  const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = warp_index();
+  const long long item = (long long)blockIdx.x * TW_WARPS + warp;
+  const int row = (int)(item / parts);
+  if (row >= total_q) return;  // the whole warp; the others do not wait for it
   const int g = lane >> 2, c = lane & 3;
-  const int s = find_seq(cu_q, S, row);
+  const int s = find_seq_warp(cu_q, S, row, lane);
   const int kbase = __ldg(cu_k + s), kcap = __ldg(cu_k + s + 1) - kbase;
   const int32_t *irow = idx + (size_t)row * topk;
   const int steps = (topk + A4_STEP - 1) / A4_STEP;
-  const int first = blockIdx.y * TW_WARPS + warp, stride = gridDim.y * TW_WARPS;
-  uint8_t *ring = a4_smem + warp * TWB_STAGES * TWB_STAGE;
-  // copies: chunk lane % 16 of the tokens 2i + lane / 16
-  const uint8_t *keys = reinterpret_cast<const uint8_t *>(k) + (size_t)kbase * TWB_ROW +
-                        (lane & 15) * 16;
-  const uint32_t dst = smem_u32(ring) + (lane >> 4) * TWB_ROW +
-                       (((lane & 15) ^ ((lane >> 4) << 2)) << 4);
+  const int first = (int)(item - (long long)row * parts), stride = parts;
+  const uint32_t ring = smem_u32(a4_smem) + warp * 2 * TWB_STAGE;
+  // this lane's place in token g: chunks 0 and 2 from `even`, 1 and 3 from `odd`
+  const uint32_t even = g * TWB_ROW + ((g & 1) << 6) + (c << 4), odd = even ^ 64u;
+  const uint8_t *keys = reinterpret_cast<const uint8_t *>(k) + (size_t)kbase * TWB_ROW + c * 16;
   auto token = [&](int n) {
     const int e = n * A4_STEP + lane;
     return e < topk ? __ldg(irow + e) : -1;
   };
-  auto copy = [&](int &j, int stage) {  // j: this lane's token, -1 where it is none
+  // j: this lane's token, -1 where it is none; four lanes copy 64 bytes of a token together
+  auto copy = [&](int &j, uint32_t stage) {
     if (j >= kcap) {
       raise_status(status, HISA_ERR_INVALID_ARG);
       j = -1;
     }
+    const uint32_t valid = __ballot_sync(0xffffffffu, j >= 0);
+    if (valid) {
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-      const int t = __shfl_sync(0xffffffffu, j, 2 * i + (lane >> 4));
-      cp_async_16_or_zero(dst + stage * TWB_STAGE + i * 2 * TWB_ROW,
-                          keys + (size_t)(uint32_t)max(t, 0) * TWB_ROW, t >= 0);
+      for (int i = 0; i < 4; i++) {
+        const int t = __shfl_sync(0xffffffffu, j, 8 * i + g);
+        const uint8_t *src = keys + (size_t)(uint32_t)max(t, 0) * TWB_ROW;
+        const uint32_t dst = stage + i * 8 * TWB_ROW;
+        cp_async_16_or_zero(dst + even, src, t >= 0);
+        cp_async_16_or_zero(dst + odd, src + 64, t >= 0);
+        cp_async_16_or_zero(dst + even + 128, src + 128, t >= 0);
+        cp_async_16_or_zero(dst + odd + 128, src + 192, t >= 0);
+      }
     }
     cp_async_commit();
   };
-  int tok[TWB_STAGES];  // of the steps in flight, oldest first
-#pragma unroll
-  for (int i = 0; i < TWB_STAGES - 1; i++) {
-    tok[i] = token(first + i * stride);
-    copy(tok[i], i);
-  }
-  int next = token(first + (TWB_STAGES - 1) * stride);
-  uint4 qw[MT][2][4];
-  float f[MT][2];
-  const float rest = scale_rest(scale);
+  int now = token(first), next = token(first + stride);
+  copy(now, ring);
+  float f, f2;
   NegLse nl[MT][2];
+  uint4 qw[MT][2][4];
+  f = scale * LOG2E;
+  f2 = fmaf(scale, LOG2E, -f) + scale * LOG2E_LO;
 #pragma unroll
   for (int mt = 0; mt < MT; mt++)
 #pragma unroll
@@ -1141,66 +1070,69 @@ token_weights_kernel(const uint16_t *__restrict__ q, const uint16_t *__restrict_
         qw[mt][r][i] = h < H ? __ldg(reinterpret_cast<const uint4 *>(
                                          q + ((size_t)row * H + h) * KV4_DIM) + 4 * i + c)
                              : make_uint4(0u, 0u, 0u, 0u);
-      f[mt][r] = scale * LOG2E;
       nl[mt][r] = neg_lse(lse, (size_t)row, H, h);
     }
-  const uint8_t *place = ring + g * TWB_ROW + ((c ^ ((g & 1) << 2)) << 4);
-  int stage = 0;
+  __syncwarp();
+  uint32_t stage = ring;
   for (int n = first; n < steps; n += stride) {
-    cp_async_wait_group<TWB_STAGES - 2>();
-    __syncwarp();  // the step has landed for every lane, and the stage before it is read
-    const int now = tok[0];
-#pragma unroll
-    for (int i = 0; i + 2 < TWB_STAGES; i++) tok[i] = tok[i + 1];
-    tok[TWB_STAGES - 2] = next;
-    copy(tok[TWB_STAGES - 2], stage == 0 ? TWB_STAGES - 1 : stage - 1);
-    next = token(n + TWB_STAGES * stride);
-    const uint8_t *at = place + stage * TWB_STAGE;
-    stage = stage == TWB_STAGES - 1 ? 0 : stage + 1;
-    if (!__any_sync(0xffffffffu, now >= 0)) continue;
-    float x[MT][4][4], v[8];
-#pragma unroll
-    for (int j = 0; j < 4; j++)
+    __syncwarp();  // every lane has read the stage that is filled now
+    const uint32_t other = ring + (stage == ring ? TWB_STAGE : 0);
+    int then = next;
+    copy(then, other);
+    next = token(n + 2 * stride);
+    cp_async_wait_group<1>();
+    __syncwarp();  // the step has landed for every lane
+    if (__any_sync(0xffffffffu, now >= 0)) {
+      float x[MT][4][4], v[8];
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        // chunk 4i + c of an odd token is at (4i + c) ^ 4: the neighbouring pair's place
-        const uint4 kw = *reinterpret_cast<const uint4 *>(
-            at + j * 8 * TWB_ROW + ((i >> 1) << 7) + ((i & 1) ? ((g & 1) ? -64 : 64) : 0));
 #pragma unroll
-        for (int mt = 0; mt < MT; mt++) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_bf16(d, qw[mt][0][i].x, qw[mt][1][i].x, qw[mt][0][i].y, qw[mt][1][i].y, kw.x, kw.y);
-          mma_bf16(d, qw[mt][0][i].z, qw[mt][1][i].z, qw[mt][0][i].w, qw[mt][1][i].w, kw.z, kw.w);
+        for (int j = 0; j < 4; j++) {
+          const uint4 kw = lds<uint4>(stage + j * 8 * TWB_ROW + ((i & 1) ? odd : even) +
+                                      (i >> 1) * 128);
 #pragma unroll
-          for (int u = 0; u < 4; u++) x[mt][j][u] = i == 0 ? d[u] : x[mt][j][u] + d[u];
+          for (int mt = 0; mt < MT; mt++) {
+            float d[4];
+            const uint4 a = qw[mt][0][i], b = qw[mt][1][i];
+            mma_bf16_first(d, a.x, b.x, a.y, b.y, kw.x, kw.y);
+            mma_bf16(d, a.z, b.z, a.w, b.w, kw.z, kw.w);
+#pragma unroll
+            for (int u = 0; u < 4; u += 2) {
+              float2 y = make_float2(d[u], d[u + 1]);
+              if (i > 0) y = add2(make_float2(x[mt][j][u], x[mt][j][u + 1]), y);
+              x[mt][j][u] = y.x;
+              x[mt][j][u + 1] = y.y;
+            }
+          }
         }
       }
-    weigh<MT>(x, f, rest, nl, v);
-    add_weights(v, now, weights + kbase, lane, status);
+      weigh<MT>(x, f, f2, nl, v);
+      add_weights(v, now, weights + kbase, lane, status);
+    }
+    now = then;
+    stage = other;
   }
   cp_async_wait_all();
-}
-
-// CTAs per row: enough to fill the GPU, at most one step per warp
-static int weight_splits(int total_q, int topk, int num_sms) {
-  const int steps = (topk + A4_STEP - 1) / A4_STEP, most = (steps + TW_WARPS - 1) / TW_WARPS;
-  const int want = (4 * num_sms + total_q - 1) / total_q;
-  return want < most ? want : most;
 }
 
 cudaError_t launch_token_weights(const uint16_t *q, const uint16_t *k, const int32_t *idx,
                                  const float *lse, const int32_t *cu_q, const int32_t *cu_k, int S,
                                  int total_q, int H, int topk, float scale, int64_t *weights,
                                  int num_sms, int *status, cudaStream_t st) {
-  const dim3 grid(total_q, weight_splits(total_q, topk, num_sms));
-  unsigned long long *w = reinterpret_cast<unsigned long long *>(weights);
-  constexpr size_t smem = (size_t)TW_WARPS * TWB_STAGES * TWB_STAGE;
   static std::atomic<int> attr[2][64];
   const auto fn = H <= 16 ? token_weights_kernel<1> : token_weights_kernel<2>;
-  const cudaError_t e = set_smem_once((const void *)fn, smem, attr[H > 16]);
+  const cudaError_t e = set_smem_once((const void *)fn, tw_smem(), attr[H > 16]);
   if (e != cudaSuccess) return e;
+  // parts of a row: enough for four waves of warps, each with a step at least (8 x 64 rows
+  // of 2048 tokens: 44 us with one wave, 39 with four, 45 with eight)
+  const int steps = (topk + A4_STEP - 1) / A4_STEP;
+  const int slots = num_sms * tw_ctas(H <= 16 ? 1 : 2) * TW_WARPS;
+  const int want = (4 * slots + total_q - 1) / total_q, parts = want < steps ? want : steps;
+  const long long items = (long long)total_q * parts;
   ProfScope ps(K_TOKEN_WEIGHTS, st);
-  fn<<<grid, TW_WARPS * 32, smem, st>>>(q, k, idx, lse, cu_q, cu_k, S, H, topk, scale, w, status);
+  fn<<<(unsigned)((items + TW_WARPS - 1) / TW_WARPS), TW_WARPS * 32, tw_smem(), st>>>(
+      q, k, idx, lse, cu_q, cu_k, S, total_q, parts, H, topk, scale,
+      reinterpret_cast<unsigned long long *>(weights), status);
   return cudaGetLastError();
 }
 

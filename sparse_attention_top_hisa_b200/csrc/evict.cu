@@ -393,7 +393,9 @@ struct RowArrays {
 };
 
 constexpr int ER_THREADS = 256;
-constexpr int ER_ROWS = 64;  // rows of a CTA
+// rows of a CTA and pieces of a thread in flight (16 sequences of up to 32768 tokens with
+// their selection: 43 us with 128 and 4, 51 with 64 and 4, 52 with 256 and 8)
+constexpr int ER_ROWS = 128, ER_UNROLL = 4;
 
 struct EvictSeq {
   int sbase, dbase, scap, n;
@@ -419,16 +421,30 @@ __device__ __forceinline__ EvictSeq evict_seq(const int32_t *cu_src, const int32
   return r;
 }
 
+// Rows rows[0 .. n) of the source to drow, drow + 1, ...: ER_UNROLL pieces of a thread are
+// read before any is written.
 template <typename T>
-__device__ __forceinline__ void move_rows(const uint8_t *src, uint8_t *dst, int bytes,
-                                          const int *rows, int n, size_t sbase, size_t drow) {
-  const int per = bytes / (int)sizeof(T);
-  const T *s = reinterpret_cast<const T *>(src);
-  T *d = reinterpret_cast<T *>(dst);
-  for (int x = threadIdx.x; x < n * per; x += ER_THREADS) {
-    const int r = x / per, p = x - r * per;
-    const int from = rows[r];
-    if (from >= 0) d[(drow + r) * per + p] = __ldg(s + (sbase + from) * per + p);
+__device__ __forceinline__ void move_rows(const uint8_t *src, uint8_t *dst, int per, const int *rows,
+                                          int n, size_t sbase, size_t drow) {
+  const T *s = reinterpret_cast<const T *>(src) + sbase * per;
+  T *d = reinterpret_cast<T *>(dst) + drow * per;
+  const int total = n * per;
+  for (int x0 = threadIdx.x; x0 < total; x0 += ER_UNROLL * ER_THREADS) {
+    T v[ER_UNROLL];
+    bool ok[ER_UNROLL];
+#pragma unroll
+    for (int u = 0; u < ER_UNROLL; u++) {
+      const int x = x0 + u * ER_THREADS;
+      ok[u] = false;
+      if (x < total) {
+        const int r = x / per, from = rows[r];
+        ok[u] = from >= 0;
+        if (ok[u]) v[u] = __ldg(s + (size_t)from * per + (x - r * per));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < ER_UNROLL; u++)
+      if (ok[u]) d[x0 + u * ER_THREADS] = v[u];
   }
 }
 
@@ -451,11 +467,11 @@ evict_rows_kernel(const __grid_constant__ RowArrays a, const int32_t *__restrict
   for (int k = 0; k < a.n; k++) {
     const size_t sb = (size_t)q.sbase, d = (size_t)q.dbase + r0;
     if (a.vec[k] == 16)
-      move_rows<uint4>(a.src[k], a.dst[k], a.bytes[k], rows, n, sb, d);
+      move_rows<uint4>(a.src[k], a.dst[k], a.bytes[k] / 16, rows, n, sb, d);
     else if (a.vec[k] == 8)
-      move_rows<uint2>(a.src[k], a.dst[k], a.bytes[k], rows, n, sb, d);
+      move_rows<uint2>(a.src[k], a.dst[k], a.bytes[k] / 8, rows, n, sb, d);
     else
-      move_rows<uint32_t>(a.src[k], a.dst[k], a.bytes[k], rows, n, sb, d);
+      move_rows<uint32_t>(a.src[k], a.dst[k], a.bytes[k] / 4, rows, n, sb, d);
   }
 }
 

@@ -7,14 +7,17 @@
 // lies at 7 * (a 5-bit number) and one of x / s at s * (a 4-bit number): both are 8-bit
 // numbers, so a quotient that is not a tie is at least 2^-8 (relative) from one, and the
 // correctly rounded fp32 quotient falls on the right side.  For x / s the product with
-// the rounded reciprocal of s is taken instead and rounded to a multiple of 2^-12 first,
-// which puts ties back where they belong and moves nothing else across one.
+// the rounded reciprocal of s is taken instead and rounded to a multiple of 2^-12 first
+// (in the FMA that adds 3072), which puts ties back where they belong and moves nothing
+// else across one; a second sum rounds to a whole number.
 //
-// A sequence with fewer live tokens than query rows is skipped whole, like one whose
-// region or length does not fit (locate).
+// A sequence whose region or length does not fit, or with fewer live tokens than query
+// rows, is skipped whole.
 //
 // One thread per group (16 per row, 8 of the key and 8 of the value): a store reads 512
-// bytes per row and writes 144, a load the reverse, so both are bound by memory.
+// bytes per row and writes 144, a load the reverse, so both are bound by memory (86 MB each
+// for 131072 rows; a plain copy of the card moves 6.0 TB/s at this size).  A warp takes 2
+// rows, or 4 where there are rows enough for every SM, whose loads are in flight together.
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"
@@ -22,8 +25,7 @@
 
 namespace hisa {
 
-constexpr int KVS_THREADS = 256;
-constexpr int KVS_ROWS = KVS_THREADS / KV4_NS;  // rows of a CTA
+constexpr int KVS_THREADS = 128, KVS_WARPS = KVS_THREADS / 32;
 
 // e5m3 byte of t >= 0 (finite), rounded to nearest even, at most 896 (byte 198)
 __device__ __forceinline__ uint32_t e5m3_round(float t) {
@@ -42,102 +44,180 @@ __device__ __forceinline__ float e5m3_value(uint32_t b) {
   return __half2float(__ushort_as_half((unsigned short)(b << 7)));
 }
 
-__device__ __forceinline__ QueryInfo locate_new(const int32_t *cu_q, const int32_t *cu_k,
-                                                const int32_t *seqlens, int S, int row,
-                                                int *status) {
-  QueryInfo r = locate(cu_q, cu_k, seqlens, S, row, status);
-  if (r.ok && r.len < __ldg(cu_q + r.seq + 1) - __ldg(cu_q + r.seq)) {
-    raise_status(status, HISA_ERR_INVALID_ARG);
-    r.ok = false;
+// The cache rows of R query rows, `row`, `row` + 2, ... (row is a warp's first for its lanes
+// 0-15 and the one after for the others): -1 where the sequence is skipped or there is none.
+template <int R>
+__device__ __forceinline__ void cache_rows(const int32_t *cu_q, const int32_t *cu_k,
+                                           const int32_t *seqlens, int S, int row, int total_q,
+                                           int *status, long long (&at)[R]) {
+  const int lane = threadIdx.x & 31, first = __shfl_sync(0xffffffffu, row, 0);
+  int s = 0, q0 = 0, q1 = 0, k0 = 0, cap = 0, len = 0;
+#pragma unroll
+  for (int i = 0; i < 2 * R; i++) {  // the warp's rows in order
+    const int r = first + i;
+    if (r >= total_q) {
+      if (lane / 16 == i % 2) at[i / 2] = -1;
+      continue;
+    }
+    if (i == 0 || r >= q1) {
+      s = find_seq_warp(cu_q, S, r, lane);
+      q0 = __ldg(cu_q + s);
+      q1 = __ldg(cu_q + s + 1);
+      k0 = __ldg(cu_k + s);
+      cap = __ldg(cu_k + s + 1) - k0;
+      len = seqlens ? __ldg(seqlens + s) : cap;
+    }
+    bool ok = true;
+    if (k0 % BLK != 0) {
+      raise_status(status, HISA_ERR_UNALIGNED);
+      ok = false;
+    } else if (len < 0 || len > cap || len < q1 - q0 || r < q0 || r >= q1) {
+      raise_status(status, HISA_ERR_INVALID_ARG);
+      ok = false;
+    }
+    if (lane / 16 == i % 2) at[i / 2] = ok ? (long long)k0 + (len - (q1 - q0) + (r - q0)) : -1;
   }
-  return r;
 }
 
+template <int R>
 __global__ void __launch_bounds__(KVS_THREADS)
 kv4_store_kernel(const uint16_t *__restrict__ k_new, const uint16_t *__restrict__ v_new,
                  const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k,
                  const int32_t *__restrict__ seqlens, int S, int total_q,
                  uint8_t *__restrict__ kv4, uint8_t *__restrict__ kv4_scale, int *status) {
-  const int row = blockIdx.x * KVS_ROWS + threadIdx.x / KV4_NS, g = threadIdx.x % KV4_NS;
-  if (row >= total_q) return;
-  const QueryInfo qi = locate_new(cu_q, cu_k, seqlens, S, row, status);
-  if (!qi.ok) return;
-  const uint4 *src = reinterpret_cast<const uint4 *>(
-      (g < 8 ? k_new : v_new) + (size_t)row * KV4_DIM + (g & 7) * KV4_GROUP);
-  const uint4 a = __ldg(src), b = __ldg(src + 1);
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint32_t mx = 0;
+  const int lane = threadIdx.x & 31, g = lane % KV4_NS;
+  const int row = (blockIdx.x * KVS_WARPS + threadIdx.x / 32) * 2 * R + lane / 16;
+  const uint4 *from = reinterpret_cast<const uint4 *>((g < 8 ? k_new : v_new) +
+                                                      (size_t)row * KV4_DIM + (g & 7) * KV4_GROUP);
+  uint4 x[R][2];
 #pragma unroll
-  for (int i = 0; i < 8; i++) mx = __vmaxu2(mx, w[i] & 0x7FFF7FFFu);
-  mx = max(mx & 0xFFFFu, mx >> 16);
-  const size_t dst = (size_t)(qi.kbase + qi.pos);
-  uint32_t byte, lo = 0x88888888u, hi = 0x88888888u;
-  if (mx >= 0x7F80u) {  // an infinity or a NaN: the group reads back as NaN
-    byte = 255u;
-    raise_status(status, HISA_ERR_INVALID_ARG);
-  } else {
-    byte = e5m3_round(__fdiv_rn(__uint_as_float(mx << 16), 7.f));
-    const float s = e5m3_value(byte);
-    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-    uint32_t c[2] = {0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 16; i++) {
-      const float x = (i & 1) ? bf_hi(w[i >> 1]) : bf_lo(w[i >> 1]);
-      float t = fmaf(x, r, 3072.f) - 3072.f;  // multiples of 2^-12
-      t = fminf(fmaxf(t, -7.f), 7.f) + 12582912.f;  // 1.5 * 2^23: rounds to a whole number
-      c[i >> 3] |= ((__float_as_uint(t) + 8u) & 15u) << (4 * (i & 7));
+  for (int i = 0; i < R; i++) {
+    x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (row + 2 * i < total_q) {
+      x[i][0] = __ldg(from + (size_t)i * 2 * (KV4_DIM / 8));
+      x[i][1] = __ldg(from + (size_t)i * 2 * (KV4_DIM / 8) + 1);
     }
-    lo = c[0];
-    hi = c[1];
   }
-  *reinterpret_cast<uint2 *>(kv4 + dst * KV4_ROW + g * 8) = make_uint2(lo, hi);
-  kv4_scale[dst * KV4_NS + g] = (uint8_t)byte;
+  long long dst[R];
+  cache_rows<R>(cu_q, cu_k, seqlens, S, row, total_q, status, dst);
+#pragma unroll
+  for (int i = 0; i < R; i++) {
+    if (dst[i] < 0) continue;
+    const uint4 a = x[i][0], b = x[i][1];
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t mx = 0;
+#pragma unroll
+    for (int j = 0; j < 8; j++) mx = __vmaxu2(mx, w[j] & 0x7FFF7FFFu);
+    mx = max(mx & 0xFFFFu, mx >> 16);
+    uint32_t byte, c[2] = {0x88888888u, 0x88888888u};
+    if (mx >= 0x7F80u) {  // an infinity or a NaN: the group reads back as NaN
+      byte = 255u;
+      raise_status(status, HISA_ERR_INVALID_ARG);
+    } else {
+      byte = e5m3_round(__fdiv_rn(__uint_as_float(mx << 16), 7.f));
+      const float s = e5m3_value(byte);
+      const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+      // |x / s| < 7.5 by the choice of s, but for the largest and the subnormal scales
+      const bool clamp = byte < 8u || byte == 198u;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        uint32_t sum = 0;
+#pragma unroll
+        for (int j = 7; j >= 0; j--) {
+          const uint32_t x2 = w[4 * h + (j >> 1)];
+          float t = fmaf((j & 1) ? bf_hi(x2) : bf_lo(x2), r, 3072.f);  // multiples of 2^-12
+          if (clamp) t = fminf(fmaxf(t, 3065.f), 3079.f);
+          // 1.5 * 2^23 + 8 + q: rounds to a whole number, whose bits are a constant and q + 8
+          t += 12582912.f + 8.f - 3072.f;
+          sum = sum * 16u + __float_as_uint(t);
+        }
+        c[h] = sum - 0x11111111u * 0x4B400000u;
+      }
+    }
+    *reinterpret_cast<uint2 *>(kv4 + (size_t)dst[i] * KV4_ROW + g * 8) = make_uint2(c[0], c[1]);
+    kv4_scale[(size_t)dst[i] * KV4_NS + g] = (uint8_t)byte;
+  }
 }
 
+template <int R>
 __global__ void __launch_bounds__(KVS_THREADS)
 kv4_load_kernel(const uint8_t *__restrict__ kv4, const uint8_t *__restrict__ kv4_scale,
                 const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k,
                 const int32_t *__restrict__ seqlens, int S, int total_q,
                 uint16_t *__restrict__ k_out, uint16_t *__restrict__ v_out, int *status) {
-  const int row = blockIdx.x * KVS_ROWS + threadIdx.x / KV4_NS, g = threadIdx.x % KV4_NS;
-  if (row >= total_q) return;
-  const QueryInfo qi = locate_new(cu_q, cu_k, seqlens, S, row, status);
-  uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-  if (qi.ok) {
-    const size_t src = (size_t)(qi.kbase + qi.pos);
-    const uint2 c = __ldg(reinterpret_cast<const uint2 *>(kv4 + src * KV4_ROW + g * 8));
-    const float s = e5m3_value(__ldg(kv4_scale + src * KV4_NS + g));
+  const int lane = threadIdx.x & 31, g = lane % KV4_NS;
+  const int row = (blockIdx.x * KVS_WARPS + threadIdx.x / 32) * 2 * R + lane / 16;
+  long long src[R];
+  cache_rows<R>(cu_q, cu_k, seqlens, S, row, total_q, status, src);
+  uint2 c[R];
+  uint32_t b[R];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      const uint32_t w = (i < 4 ? c.x : c.y) >> (8 * (i & 3));
-      const float x = (float)((int)(w & 15u) - 8) * s, y = (float)((int)((w >> 4) & 15u) - 8) * s;
-      const __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
-      o[i] = *reinterpret_cast<const uint32_t *>(&p);
+  for (int i = 0; i < R; i++) {
+    c[i] = make_uint2(0x88888888u, 0x88888888u);  // zeros
+    b[i] = 0;
+    if (src[i] >= 0) {
+      c[i] = __ldg(reinterpret_cast<const uint2 *>(kv4 + (size_t)src[i] * KV4_ROW + g * 8));
+      b[i] = __ldg(kv4_scale + (size_t)src[i] * KV4_NS + g);
     }
   }
-  uint4 *dst = reinterpret_cast<uint4 *>((g < 8 ? k_out : v_out) + (size_t)row * KV4_DIM +
-                                         (g & 7) * KV4_GROUP);
-  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  uint4 *to = reinterpret_cast<uint4 *>((g < 8 ? k_out : v_out) + (size_t)row * KV4_DIM +
+                                        (g & 7) * KV4_GROUP);
+#pragma unroll
+  for (int i = 0; i < R; i++) {
+    if (row + 2 * i >= total_q) continue;
+    const __nv_bfloat162 s = __float2bfloat162_rn(e5m3_value(b[i]));
+    uint32_t o[8];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      // nibbles j and j + 4 of the word as 128 + u in bf16; minus 136 and times s, both exact
+      uint32_t e[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const uint32_t t = (((h ? c[i].y : c[i].x) >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
+        const __nv_bfloat162 v =
+            __hmul2(__hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&t),
+                            __float2bfloat162_rn(-136.f)), s);
+        e[j] = *reinterpret_cast<const uint32_t *>(&v);
+      }
+      o[4 * h] = __byte_perm(e[0], e[1], 0x5410);
+      o[4 * h + 1] = __byte_perm(e[2], e[3], 0x5410);
+      o[4 * h + 2] = __byte_perm(e[0], e[1], 0x7632);
+      o[4 * h + 3] = __byte_perm(e[2], e[3], 0x7632);
+    }
+    to[(size_t)i * 2 * (KV4_DIM / 8)] = make_uint4(o[0], o[1], o[2], o[3]);
+    to[(size_t)i * 2 * (KV4_DIM / 8) + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// Rows of a warp: 4 once that still leaves two CTAs for every SM (16 rows of a CTA).  Stored
+// and read back, 131072 rows take 42 us with 2, 39 with 4 and 43 with 8.
+static int rows_per_unit(int total_q, int num_sms) { return total_q >= 32 * num_sms ? 2 : 1; }
+static int store_grid(int total_q, int r) {
+  const int per = KVS_WARPS * 2 * r;
+  return (total_q + per - 1) / per;
 }
 
 cudaError_t launch_kv4_store(const uint16_t *k_new, const uint16_t *v_new, const int32_t *cu_q,
                              const int32_t *cu_k, const int32_t *seqlens, int S, int total_q,
-                             uint8_t *kv4, uint8_t *kv4_scale, int *status, cudaStream_t st) {
-  const int grid = (total_q + KVS_ROWS - 1) / KVS_ROWS;
+                             uint8_t *kv4, uint8_t *kv4_scale, int num_sms, int *status,
+                             cudaStream_t st) {
+  const int r = rows_per_unit(total_q, num_sms);
   ProfScope ps(K_KV4_STORE, st);
-  kv4_store_kernel<<<grid, KVS_THREADS, 0, st>>>(k_new, v_new, cu_q, cu_k, seqlens, S, total_q,
-                                                 kv4, kv4_scale, status);
+  const auto fn = r == 2 ? kv4_store_kernel<2> : kv4_store_kernel<1>;
+  fn<<<store_grid(total_q, r), KVS_THREADS, 0, st>>>(k_new, v_new, cu_q, cu_k, seqlens, S, total_q,
+                                                     kv4, kv4_scale, status);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_load(const uint8_t *kv4, const uint8_t *kv4_scale, const int32_t *cu_q,
                             const int32_t *cu_k, const int32_t *seqlens, int S, int total_q,
-                            uint16_t *k_out, uint16_t *v_out, int *status, cudaStream_t st) {
-  const int grid = (total_q + KVS_ROWS - 1) / KVS_ROWS;
+                            uint16_t *k_out, uint16_t *v_out, int num_sms, int *status,
+                            cudaStream_t st) {
+  const int r = rows_per_unit(total_q, num_sms);
   ProfScope ps(K_KV4_LOAD, st);
-  kv4_load_kernel<<<grid, KVS_THREADS, 0, st>>>(kv4, kv4_scale, cu_q, cu_k, seqlens, S, total_q,
-                                                k_out, v_out, status);
+  const auto fn = r == 2 ? kv4_load_kernel<2> : kv4_load_kernel<1>;
+  fn<<<store_grid(total_q, r), KVS_THREADS, 0, st>>>(kv4, kv4_scale, cu_q, cu_k, seqlens, S,
+                                                     total_q, k_out, v_out, status);
   return cudaGetLastError();
 }
 
