@@ -384,7 +384,9 @@ hisa_status hisa_kv4_load(const uint8_t *kv4, const uint8_t *kv4_scale,
  *   weights        int64 [rows_k] or NULL: the accumulated attention weight of every token,
  *   (in/out)       in units of 2^-32.  The weight of each selected token, summed over the
  *                  heads, is rounded to a whole unit and added; integer sums make the
- *                  result independent of the order of the additions.  Not cleared here.
+ *                  result independent of the order of the additions.  Not cleared here.  A
+ *                  weight that is not a number adds nothing and raises
+ *                  HISA_ERR_INVALID_ARG in the device status word.
  * Every other argument and the errors are those of hisa_sparse_attention.  out must be
  * 16-byte aligned.
  * Precision: q.k are sums of exact products in fp32 (a value of q more than 2^28 times
@@ -430,8 +432,8 @@ hisa_status hisa_token_weights(const hisa_bf16 *q_att, const hisa_bf16 *k_att,
  *                  of the i-th token that stays, ascending; entries past the count are left
  *                  as they were.
  *   kept_len (out) int32 [num_seqs]: the count, min(len_s, keep[s]).
- * A sequence with a negative budget, or with a length outside its region or above
- * max_seqlen_k, gets kept_len -1 and raises HISA_ERR_INVALID_ARG in the device status word.
+ * max_seqlen_k is at most 2^30.  A sequence with a negative budget, or with a length
+ * outside its region or above max_seqlen_k, gets kept_len -1 and raises HISA_ERR_INVALID_ARG in the device status word.
  */
 hisa_status hisa_evict_select(const int64_t *weights, const int32_t *cu_seqlens_k,
                               const int32_t *seqlens_k, const int32_t *keep, int num_seqs,

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -526,9 +527,9 @@ def hisa_kv4_load(kv4: torch.Tensor, kv4_scale: torch.Tensor, cu_seqlens_q: torc
     n = None if seqlens_k is None else _at(seqlens_k, "seqlens_k", i32, dev)
     S = _seqs(cu_seqlens_q, cu_seqlens_k, seqlens_k)
     if k_out is None:
-        k_out = torch.empty((total_q, HISA_ATT_DIM), dtype=torch.bfloat16, device=kv4.device)
+        k_out = kv4.new_empty((total_q, HISA_ATT_DIM), dtype=torch.bfloat16)
     if v_out is None:
-        v_out = torch.empty((total_q, HISA_ATT_DIM), dtype=torch.bfloat16, device=kv4.device)
+        v_out = torch.empty_like(k_out)
     k = _at(k_out, "k_out", torch.bfloat16, dev, HISA_ATT_DIM)
     v = _at(v_out, "v_out", torch.bfloat16, dev, HISA_ATT_DIM)
     if k_out.shape[0] != total_q or v_out.shape[0] != total_q:
@@ -588,8 +589,8 @@ def hisa_sparse_attention_kv4(q_att: torch.Tensor, kv4: torch.Tensor, kv4_scale:
         if lse is None:
             raise ValueError("weights need lse")
         w = _at(weights, "weights", torch.int64, dev)
-    _check(lib().hisa_sparse_attention_kv4(q, a, b, idx, cq, ck, S, total_q, heads, k, scale, o,
-                                           ls, w, _raw_stream(stream, dev)),
+    _check(lib().hisa_sparse_attention_kv4(q, a, b, idx, cq, ck, S, total_q, heads, k,
+                                           float(scale), o, ls, w, _raw_stream(stream, dev)),
            "hisa_sparse_attention_kv4")
     return out
 
@@ -609,8 +610,8 @@ def hisa_token_weights(q_att: torch.Tensor, k_att: torch.Tensor, topk_idx: torch
     w = _at(weights, "weights", torch.int64, dev)
     total_q, heads, k = _att_shapes(q_att, topk_idx, lse, weights, k_att.shape[0])
     S = _seqs(cu_seqlens_q, cu_seqlens_k, None)
-    _check(lib().hisa_token_weights(q, ka, idx, ls, cq, ck, S, total_q, heads, k, scale, w,
-                                    _raw_stream(stream, dev)), "hisa_token_weights")
+    _check(lib().hisa_token_weights(q, ka, idx, ls, cq, ck, S, total_q, heads, k, float(scale),
+                                    w, _raw_stream(stream, dev)), "hisa_token_weights")
     return weights
 
 
@@ -645,9 +646,6 @@ class _Rows(ctypes.Structure):
                 ("row_bytes", ctypes.c_size_t)]
 
 
-_RowArray = _Rows * HISA_MAX_ROW_ARRAYS
-
-
 def hisa_evict_rows(src, dst, cu_src: torch.Tensor, cu_dst: torch.Tensor, kept: torch.Tensor,
                     kept_len: torch.Tensor, max_keep: int, stream=None) -> None:
     """Move the rows that stay (kept, kept_len of hisa_evict_select) of the row arrays src to
@@ -658,31 +656,36 @@ def hisa_evict_rows(src, dst, cu_src: torch.Tensor, cu_dst: torch.Tensor, kept: 
     ks, kn = _at(kept, "kept", i32, dev), _at(kept_len, "kept_len", i32, dev)
     cs, cd = _at(cu_src, "cu_src", i32, dev), _at(cu_dst, "cu_dst", i32, dev)
     S, n_rows = _seqs(cu_dst, cu_src, kept_len), kept.numel()
-    rows = _RowArray()
-    spans = []  # first and last byte behind, destinations and sources; in place counts once
-    for i, (a, b) in enumerate(zip(src, dst)):
+    rows = []  # source, destination and bytes of a row, as the C structure has them
+    # first byte, last byte behind, whether a destination; in place counts once
+    spans = [(ks, ks + 4 * n_rows, False), (kn, kn + 4 * S, False)]
+    for a, b in zip(src, dst):
         dt = a.dtype
-        pa, pb = _at(a, "a source", dt, dev), _at(b, "a destination", b.dtype, dev)
-        sa, sb = a.shape, b.shape
-        if dt is not b.dtype or not sa or len(sa) != len(sb) or sa[1:] != sb[1:]:
+        pa = _at(a, "a source", dt, dev)
+        pb = pa if b is a else _at(b, "a destination", b.dtype, dev)
+        sa, sb, na, nb = a.shape, b.shape, a.numel(), b.numel()
+        if not sa or not sb or b.dtype is not dt:
             raise ValueError("a source and its destination must have rows of one type and shape")
         if sa[0] != n_rows:
             raise ValueError("kept must hold one number per source row")
-        nbytes = a.nbytes
-        row = nbytes // n_rows if n_rows else 4
-        r = rows[i]
-        r.src, r.dst, r.row_bytes = pa, pb, row
-        spans.append((pb, pb + b.nbytes, 1))
-        if pa != pb or sa != sb:
-            spans.append((pa, pa + nbytes, 0))
+        width = na // n_rows if n_rows else 1
+        if width * sb[0] != nb:
+            raise ValueError("a source and its destination must have rows of one type and shape")
+        size = dt.itemsize
+        rows += (pa, pb, width * size)
+        spans.append((pb, pb + nb * size, True))
+        if pa != pb or na != nb:
+            spans.append((pa, pa + na * size, False))
     # in order of their starts, a span may touch none before it, unless both are sources
     spans.sort()
     end = end_dst = 0
     for a, b, is_dst in spans:
         if a < (end if is_dst else end_dst) and a < b:
-            raise ValueError("a destination overlaps a source, or two destinations overlap")
-        end = max(end, b)
-        if is_dst:
-            end_dst = max(end_dst, b)
+            raise ValueError("a destination overlaps a source or kept, or two destinations overlap")
+        if b > end:
+            end = b
+        if is_dst and b > end_dst:
+            end_dst = b
+    rows = struct.pack(f"{len(rows)}Q", *rows)
     _check(lib().hisa_evict_rows(rows, len(src), cs, cd, ks, kn, S, int(max_keep),
                                  _raw_stream(stream, dev)), "hisa_evict_rows")

@@ -604,7 +604,8 @@ hisa_status hisa_evict_select(const int64_t *weights, const int32_t *cu_seqlens_
                               const int32_t *seqlens_k, const int32_t *keep, int num_seqs,
                               int max_seqlen_k, int n_sink, int n_recent, int32_t *kept,
                               int32_t *kept_len, hisa_stream_t stream) {
-  if (num_seqs < 0 || max_seqlen_k < 0 || n_sink < 0 || n_recent < 0) return HISA_ERR_INVALID_ARG;
+  if (num_seqs < 0 || max_seqlen_k < 0 || max_seqlen_k > (1 << 30) || n_sink < 0 || n_recent < 0)
+    return HISA_ERR_INVALID_ARG;
   if (num_seqs == 0) return HISA_OK;
   if (!weights || !cu_seqlens_k || !keep || !kept || !kept_len) return HISA_ERR_INVALID_ARG;
   if (!aligned(weights, 8) || !aligned(cu_seqlens_k, 4) || !aligned(seqlens_k, 4) ||

@@ -310,3 +310,80 @@ def test_prefill_evict_decode():
         ref.check_out(f64(out), np.abs(vr).max())
         ref.check_lse(f64(lse))
     assert h.hisa_device_status() == 0
+
+
+def test_kept_may_not_be_overwritten():
+    h = H()
+    cu = dev_i32([0, 128])
+    kept, n = torch.arange(128, dtype=torch.int32, device="cuda"), dev_i32([1])
+    for arrays in ([kept], [n]):
+        with pytest.raises(ValueError, match="kept"):
+            h.hisa_evict_rows([torch.zeros(128, dtype=torch.int32, device="cuda")], arrays, cu, cu,
+                              kept, n, 1)
+
+
+def test_lengths_past_the_limit_are_refused():
+    h = H()
+    w = torch.zeros(128, dtype=torch.int64, device="cuda")
+    with pytest.raises(h.HisaError):
+        h.hisa_evict_select(w, dev_i32([0, 128]), None, dev_i32([5]), (1 << 30) + 1, 0, 0)
+
+
+@pytest.mark.parametrize("seqs,top", [(1, 40000), (3, 33000), (20, 17000), (100, 9000), (160, 700)])
+def test_select_every_split_of_a_sequence(seqs, top):
+    """One to eight CTAs per sequence, keys in registers or read again, odd lengths."""
+    rng = np.random.Generator(np.random.PCG64(seqs))
+    lens = (top - rng.integers(0, top // 2, seqs)).tolist()
+    lens[0] = top
+    keep = [int(rng.integers(0, n + 1)) for n in lens]
+    cu_k = regions(lens)
+    w = weights_of("real", int(cu_k[-1]), rng)
+    w[: top // 3] //= 1 << 30  # ties in the first sequence
+    kept, n = run_select(w, cu_k, lens, keep, 7, 100)
+    for s, length in enumerate(lens):
+        c, b = int(cu_k[s]), keep[s]
+        sink = min(7, b)
+        recent = min(100, b - sink)
+        if length <= b:
+            want = np.arange(length)
+        else:
+            x = w[c + sink:c + length - recent]
+            free = np.argsort(-x, kind="stable")[:b - sink - recent] + sink
+            want = np.sort(np.concatenate([np.arange(sink), free,
+                                           np.arange(length - recent, length)]))
+        assert n[s] == len(want) and np.array_equal(kept[c:c + len(want)], want)
+
+
+def test_select_and_move_in_a_graph():
+    """Captured once, replayed on changed weights and lengths."""
+    h = H()
+    rng = np.random.Generator(np.random.PCG64(6))
+    cu = regions([3000, 3000])
+    rows = int(cu[-1])
+    c, keep = dev_i32(cu), dev_i32([500, 700])
+    w = torch.zeros(rows, dtype=torch.int64, device="cuda")
+    lens, x = dev_i32([3000, 3000]), torch.zeros(rows, 8, dtype=torch.int32, device="cuda")
+    kept = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    n = torch.zeros(2, dtype=torch.int32, device="cuda")
+
+    def step():
+        h.hisa_evict_select(w, c, lens, keep, 3000, 4, 64, kept=kept, kept_len=n)
+        h.hisa_evict_rows([x], [x], c, c, kept, n, 700)
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(3):
+        hw = weights_of("real", rows, rng)
+        hl = rng.integers(300, 3001, 2)
+        hx = rng.integers(0, 1 << 30, (rows, 8)).astype(np.int32)
+        w.copy_(torch.from_numpy(hw))
+        lens.copy_(torch.from_numpy(hl.astype(np.int32)))
+        x.copy_(torch.from_numpy(hx))
+        g.replay()
+        torch.cuda.synchronize()
+        for s in range(2):
+            at = int(cu[s])
+            want = kv4_ref.evict_select(hw[at:at + hl[s]], int(hl[s]), [500, 700][s], 4, 64)
+            assert int(n[s]) == len(want)
+            assert np.array_equal(x[at:at + len(want)].cpu().numpy(), hx[at + want])

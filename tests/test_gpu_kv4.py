@@ -436,3 +436,128 @@ def test_binding_refusals():
         h.hisa_kv4_store(bf16(np.ones((2, DIM))), bf16(np.ones((3, DIM))), cu_q, cu_k, None, *dev)
     with pytest.raises(ValueError, match="sequences"):
         h.hisa_kv4_load(*dev, cu_q, cu_k, dev_i32([1, 2]), 2)
+
+
+@pytest.mark.parametrize("seqs", [31, 33, 129, 700])
+def test_many_sequences(seqs):
+    """Rows find their sequence among many, empty ones and ones without queries among them."""
+    h = H()
+    rng = np.random.Generator(np.random.PCG64(seqs))
+    lens = rng.integers(0, 60, seqs)
+    news = [int(rng.integers(0, min(4, n) + 1)) if n else 0 for n in lens]
+    lens[-1], news[-1] = 40, 0
+    c = Case(seqs, 6, 24, lens.tolist(), news, empty=5)
+    c.check()
+    cu_q, cu_k, n = c.cu_q, c.cu_k, int(c.cu_q[-1])
+    k, v = bf16(hard_rows(n, rng)), bf16(hard_rows(n, rng))
+    kv4 = torch.zeros(c.rows, 128, dtype=torch.uint8, device="cuda")
+    sc = torch.zeros(c.rows, 16, dtype=torch.uint8, device="cuda")
+    args = dev_i32(cu_q), dev_i32(cu_k), dev_i32(lens)
+    h.hisa_device_status(clear=True)
+    h.hisa_kv4_store(k, v, *args, kv4, sc)
+    kb, vb = h.hisa_kv4_load(kv4, sc, *args, n)
+    assert h.hisa_device_status() == 0
+    codes, scales = kv4_ref.pack(*kv4_ref.quantise(f64(k)), *kv4_ref.quantise(f64(v)))
+    at = new_rows(lens.tolist(), news, cu_k)
+    assert np.array_equal(kv4.cpu().numpy()[at], codes)
+    assert np.array_equal(sc.cpu().numpy()[at], scales)
+    assert int((sc.cpu().numpy() != 0).any(1).sum()) <= n
+    kr, vr = kv4_ref.values(codes, scales)
+    assert np.array_equal(f64(kb), kr) and np.array_equal(f64(vb), vr)
+    # the bf16 token weights look their rows up the same way
+    keys = bf16(rng.standard_normal((c.rows, DIM)))
+    lse = torch.empty(n, 6, device="cuda")
+    h.hisa_sparse_attention(c.q, keys, keys, dev_i32(c.idx), args[0], args[1], c.scale, lse=lse)
+    w = torch.zeros(c.rows, dtype=torch.int64, device="cuda")
+    h.hisa_token_weights(c.q, keys, dev_i32(c.idx), lse, args[0], args[1], c.scale, w)
+    ref = kv4_ref.Attention(f64(c.q), f64(keys), None, c.idx, cu_q, cu_k,
+                            np.float64(np.float32(c.scale)))
+    ref.check_weights(w.cpu().numpy(), c.rows)
+
+
+@pytest.mark.parametrize("rows", [1183, 4800, 9473])
+def test_store_many_rows(rows):
+    """Enough rows for several per thread, in a chunk that ends anywhere: the last warp is
+    part empty, two sequences meet inside one."""
+    h = H()
+    rng = np.random.Generator(np.random.PCG64(rows))
+    lens, news = [rows, 700], [rows - 333, 333]
+    cu_q, cu_k = layout(lens, news)
+    k, v = bf16(hard_rows(rows, rng)), bf16(hard_rows(rows, rng))
+    kv4 = torch.full((int(cu_k[-1]), 128), 7, dtype=torch.uint8, device="cuda")
+    sc = torch.full((int(cu_k[-1]), 16), 7, dtype=torch.uint8, device="cuda")
+    args = dev_i32(cu_q), dev_i32(cu_k), dev_i32(lens)
+    h.hisa_kv4_store(k, v, *args, kv4, sc)
+    kb, vb = h.hisa_kv4_load(kv4, sc, *args, rows)
+    codes, scales = kv4_ref.pack(*kv4_ref.quantise(f64(k)), *kv4_ref.quantise(f64(v)))
+    want = np.full((int(cu_k[-1]), 128), 7, np.uint8), np.full((int(cu_k[-1]), 16), 7, np.uint8)
+    at = new_rows(lens, news, cu_k)
+    want[0][at], want[1][at] = codes, scales
+    assert np.array_equal(kv4.cpu().numpy(), want[0]) and np.array_equal(sc.cpu().numpy(), want[1])
+    kr, vr = kv4_ref.values(codes, scales)
+    assert np.array_equal(f64(kb), kr) and np.array_equal(f64(vb), vr)
+
+
+@pytest.mark.parametrize("heads,rows,topk", [(16, 7000, 40), (9, 1500, 150), (32, 5000, 33),
+                                             (20, 900, 260)])
+def test_attention_one_warp_per_row(heads, rows, topk):
+    """Row counts at which a warp has a row to itself, not a multiple of a CTA's warps; a
+    sample of the rows against the reference, the weights' total over all."""
+    rng = np.random.Generator(np.random.PCG64(rows))
+    length = 900
+    idx = np.argsort(rng.random((rows, length)), 1)[:, :topk].astype(np.int32)
+    idx[rng.random(idx.shape) < 0.1] = -1
+    idx[5] = -1
+    c = Case(rows, heads, topk, [length + rows], [rows], idx=idx)
+    h = H()
+    h.hisa_device_status(clear=True)
+    out, lse, w = c.run(True)
+    assert h.hisa_device_status() == 0
+    k, v = kv4_ref.values(c.codes, c.scales)
+    pick = np.unique(np.concatenate([np.arange(9), np.arange(rows - 9, rows),
+                                     rng.integers(0, rows, 60)]))
+    ref = kv4_ref.Attention(f64(c.q)[pick], k, v, idx[pick], np.array([0, len(pick)]), c.cu_k,
+                            np.float64(np.float32(c.scale)))
+    ref.check_out(out[pick], np.abs(v).max())
+    ref.check_lse(lse[pick])
+    n = (idx >= 0).any(1).sum()
+    assert abs(w.sum() * 2.0 ** -32 - n * heads) <= \
+        n * heads * 2.0 ** -11 + (idx >= 0).sum() * 2.0 ** -33
+    out2, lse2, w2 = c.run(True)
+    assert np.array_equal(w, w2) and np.array_equal(out, out2)
+    out3, _, _ = c.run(False)  # without weights: another kernel, the same values
+    assert np.array_equal(out, out3)
+
+
+def test_calls_on_two_streams_add_to_one_accumulator():
+    h = H()
+    c = Case(71, 16, 300, [900], [64], empty=0)
+    _, _, w1 = c.run(True)
+    dev = [torch.from_numpy(x).cuda() for x in (c.codes, c.scales)]
+    idx, cu_q, cu_k = dev_i32(c.idx), dev_i32(c.cu_q), dev_i32(c.cu_k)
+    w = torch.zeros(c.rows, dtype=torch.int64, device="cuda")
+    lse = [torch.empty(64, 16, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, x in zip(streams, lse):
+            with torch.cuda.stream(s):
+                h.hisa_sparse_attention_kv4(c.q, *dev, idx, cu_q, cu_k, c.scale, lse=x, weights=w)
+    torch.cuda.synchronize()
+    assert np.array_equal(w.cpu().numpy(), 10 * w1)
+
+
+def test_empty_calls():
+    h = H()
+    c = Case(81, 4, 8, [100], [2])
+    dev = [torch.from_numpy(x).cuda() for x in (c.codes, c.scales)]
+    cu_k, none = dev_i32(c.cu_k), dev_i32([0, 0])
+    q = torch.empty(0, 4, DIM, dtype=torch.bfloat16, device="cuda")
+    idx = torch.empty(0, 8, dtype=torch.int32, device="cuda")
+    x = torch.empty(0, DIM, dtype=torch.bfloat16, device="cuda")
+    assert h.hisa_sparse_attention_kv4(q, *dev, idx, none, cu_k, 0.1).shape == (0, 4, DIM)
+    h.hisa_kv4_store(x, x, none, cu_k, dev_i32([100]), *dev)
+    assert h.hisa_kv4_load(*dev, none, cu_k, dev_i32([100]), 0)[0].shape == (0, DIM)
+    with pytest.raises(h.HisaError):  # no entry per row at all
+        h.hisa_sparse_attention_kv4(c.q, *dev, dev_i32(np.zeros((2, 0))), dev_i32(c.cu_q), cu_k,
+                                    0.1)
