@@ -12,7 +12,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from typing import Optional
 
 import torch
@@ -453,42 +452,37 @@ def hisa_sparse_attention(q_att: torch.Tensor, k_att: torch.Tensor, v_att: torch
     return out
 
 
-# The entry points below are called once per layer and decode step, so their checks are
-# written to cost little on the host: one helper checks a tensor and gives its address,
-# and only a tensor that fails is looked at again to say why.
-
-def _device_of(t: torch.Tensor, name: str) -> int:
-    """Index of the CUDA device of t, which has to be the current one."""
-    if t is None:
-        raise ValueError(f"{name} is required")
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current device, is on {t.device}")
-    return dev
+class _Rows(ctypes.Structure):
+    """hisa_rows, for callers of lib().hisa_evict_rows."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p),
+                ("row_bytes", ctypes.c_size_t)]
 
 
-def _at(t: torch.Tensor, name: str, dtype, dev: int, cols: Optional[int] = None) -> int:
-    """Address of a tensor that is checked for device, dtype, contiguity and width."""
-    if t is None or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or \
-            (cols is not None and (t.dim() != 2 or t.shape[1] != cols)):
-        _need(t, name, dtype, cols)
-        raise ValueError(f"tensors must be on one device: {name} is on {t.device}")
-    return t.data_ptr()
+# The entry points below are called once per layer and decode step; their arguments are
+# checked in _hisa_torch (csrc/torch_binding.cpp), which calls the same C ABI.
+
+_torch_binding = None
 
 
-def _raw_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+def _raise(code: int, what: str):
+    raise HisaError(code, what)
 
 
-def _seqs(cu_q: Optional[torch.Tensor], cu_k: torch.Tensor, lens: Optional[torch.Tensor]) -> int:
-    """Number of sequences of the offsets and lengths, which have to agree on it."""
-    S = cu_k.numel() - 1
-    if S < 0 or (cu_q is not None and cu_q.numel() != S + 1) or \
-            (lens is not None and lens.numel() != S):
-        raise ValueError("cu_seqlens_q, cu_seqlens_k and seqlens_k disagree on the sequences")
-    return S
+def _native():
+    """The compiled argument checks, given the loaded library's entry points."""
+    global _torch_binding
+    if _torch_binding is None:
+        L = lib()
+        try:
+            from . import _hisa_torch as mod
+        except ImportError as e:
+            raise ImportError("_hisa_torch.so is missing or was built for another torch: build it "
+                              "with `python -m sparse_attention_top_hisa_b200.build`") from e
+        mod.setup(_raise, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+            "hisa_kv4_store", "hisa_kv4_load", "hisa_sparse_attention_kv4", "hisa_token_weights",
+            "hisa_evict_select", "hisa_evict_rows")))
+        _torch_binding = mod
+    return _torch_binding
 
 
 def hisa_kv4_store(k_new: torch.Tensor, v_new: torch.Tensor, cu_seqlens_q: torch.Tensor,
@@ -496,21 +490,8 @@ def hisa_kv4_store(k_new: torch.Tensor, v_new: torch.Tensor, cu_seqlens_q: torch
                    kv4: torch.Tensor, kv4_scale: torch.Tensor, stream=None) -> None:
     """Quantise the key and value rows of the query positions (bf16 [total_q, 128]) into the
     4-bit cache kv4 uint8 [rows, 128], kv4_scale uint8 [rows, 16]."""
-    dev, i32 = _device_of(kv4, "kv4"), torch.int32
-    a = _at(kv4, "kv4", torch.uint8, dev, HISA_KV4_ROW_BYTES)
-    b = _at(kv4_scale, "kv4_scale", torch.uint8, dev, HISA_KV4_ROW_SCALES)
-    k = _at(k_new, "k_new", torch.bfloat16, dev, HISA_ATT_DIM)
-    v = _at(v_new, "v_new", torch.bfloat16, dev, HISA_ATT_DIM)
-    cq = _at(cu_seqlens_q, "cu_seqlens_q", i32, dev)
-    ck = _at(cu_seqlens_k, "cu_seqlens_k", i32, dev)
-    n = None if seqlens_k is None else _at(seqlens_k, "seqlens_k", i32, dev)
-    S, total_q = _seqs(cu_seqlens_q, cu_seqlens_k, seqlens_k), k_new.shape[0]
-    if v_new.shape[0] != total_q:
-        raise ValueError("k_new and v_new must have the same shape")
-    if kv4.shape[0] != kv4_scale.shape[0]:
-        raise ValueError("kv4 and kv4_scale must have the same number of rows")
-    _check(lib().hisa_kv4_store(k, v, cq, ck, n, S, total_q, a, b, _raw_stream(stream, dev)),
-           "hisa_kv4_store")
+    _native().kv4_store(k_new, v_new, cu_seqlens_q, cu_seqlens_k, seqlens_k, kv4, kv4_scale,
+                        None if stream is None else stream.cuda_stream)
 
 
 def hisa_kv4_load(kv4: torch.Tensor, kv4_scale: torch.Tensor, cu_seqlens_q: torch.Tensor,
@@ -519,41 +500,8 @@ def hisa_kv4_load(kv4: torch.Tensor, kv4_scale: torch.Tensor, cu_seqlens_q: torc
                   stream=None):
     """The rows of the query positions back from the 4-bit cache; returns (k, v) bf16
     [total_q, 128]."""
-    dev, i32 = _device_of(kv4, "kv4"), torch.int32
-    a = _at(kv4, "kv4", torch.uint8, dev, HISA_KV4_ROW_BYTES)
-    b = _at(kv4_scale, "kv4_scale", torch.uint8, dev, HISA_KV4_ROW_SCALES)
-    cq = _at(cu_seqlens_q, "cu_seqlens_q", i32, dev)
-    ck = _at(cu_seqlens_k, "cu_seqlens_k", i32, dev)
-    n = None if seqlens_k is None else _at(seqlens_k, "seqlens_k", i32, dev)
-    S = _seqs(cu_seqlens_q, cu_seqlens_k, seqlens_k)
-    if k_out is None:
-        k_out = kv4.new_empty((total_q, HISA_ATT_DIM), dtype=torch.bfloat16)
-    if v_out is None:
-        v_out = torch.empty_like(k_out)
-    k = _at(k_out, "k_out", torch.bfloat16, dev, HISA_ATT_DIM)
-    v = _at(v_out, "v_out", torch.bfloat16, dev, HISA_ATT_DIM)
-    if k_out.shape[0] != total_q or v_out.shape[0] != total_q:
-        raise ValueError("k_out and v_out need one row per query row")
-    if kv4.shape[0] != kv4_scale.shape[0]:
-        raise ValueError("kv4 and kv4_scale must have the same number of rows")
-    _check(lib().hisa_kv4_load(a, b, cq, ck, n, S, int(total_q), k, v, _raw_stream(stream, dev)),
-           "hisa_kv4_load")
-    return k_out, v_out
-
-
-def _att_shapes(q_att: torch.Tensor, topk_idx: torch.Tensor, lse: Optional[torch.Tensor],
-                weights: Optional[torch.Tensor], rows: int):
-    """(total_q, H, k) of an attention's arguments, which have to fit one another."""
-    qs, ks = q_att.shape, topk_idx.shape
-    if len(qs) != 3 or qs[2] != HISA_ATT_DIM:
-        raise ValueError(f"q_att must be [total_q, H, {HISA_ATT_DIM}], got {tuple(qs)}")
-    if len(ks) != 2 or ks[0] != qs[0]:
-        raise ValueError("topk_idx must be [total_q, k]")
-    if lse is not None and lse.shape != qs[:2]:
-        raise ValueError("lse must be [total_q, H]")
-    if weights is not None and weights.numel() != rows:
-        raise ValueError("weights must hold one number per cache row")
-    return qs[0], qs[1], ks[1]
+    return _native().kv4_load(kv4, kv4_scale, cu_seqlens_q, cu_seqlens_k, seqlens_k, total_q,
+                              k_out, v_out, None if stream is None else stream.cuda_stream)
 
 
 def hisa_sparse_attention_kv4(q_att: torch.Tensor, kv4: torch.Tensor, kv4_scale: torch.Tensor,
@@ -566,33 +514,8 @@ def hisa_sparse_attention_kv4(q_att: torch.Tensor, kv4: torch.Tensor, kv4_scale:
     """Attention over each query's selected tokens of the 4-bit cache; returns out bf16
     [total_q, H, 128].  weights int64 [rows], in units of HISA_WEIGHT_UNIT: the attention
     weight of every selected token, summed over the heads, is added (needs lse)."""
-    dev, i32 = _device_of(q_att, "q_att"), torch.int32
-    q = _at(q_att, "q_att", torch.bfloat16, dev)
-    a = _at(kv4, "kv4", torch.uint8, dev, HISA_KV4_ROW_BYTES)
-    b = _at(kv4_scale, "kv4_scale", torch.uint8, dev, HISA_KV4_ROW_SCALES)
-    idx = _at(topk_idx, "topk_idx", i32, dev)
-    cq = _at(cu_seqlens_q, "cu_seqlens_q", i32, dev)
-    ck = _at(cu_seqlens_k, "cu_seqlens_k", i32, dev)
-    rows = kv4.shape[0]
-    if kv4_scale.shape[0] != rows:
-        raise ValueError("kv4 and kv4_scale must have the same number of rows")
-    total_q, heads, k = _att_shapes(q_att, topk_idx, lse, weights, rows)
-    S = _seqs(cu_seqlens_q, cu_seqlens_k, None)
-    if out is None:
-        out = torch.empty_like(q_att)
-    elif out.shape != q_att.shape:
-        raise ValueError("out must have the shape of q_att")
-    o = _at(out, "out", torch.bfloat16, dev)
-    ls = None if lse is None else _at(lse, "lse", torch.float32, dev)
-    w = None
-    if weights is not None:
-        if lse is None:
-            raise ValueError("weights need lse")
-        w = _at(weights, "weights", torch.int64, dev)
-    _check(lib().hisa_sparse_attention_kv4(q, a, b, idx, cq, ck, S, total_q, heads, k,
-                                           float(scale), o, ls, w, _raw_stream(stream, dev)),
-           "hisa_sparse_attention_kv4")
-    return out
+    return _native().attention_kv4(q_att, kv4, kv4_scale, topk_idx, cu_seqlens_q, cu_seqlens_k,
+                                   scale, out, lse, weights, None if stream is None else stream.cuda_stream)
 
 
 def hisa_token_weights(q_att: torch.Tensor, k_att: torch.Tensor, topk_idx: torch.Tensor,
@@ -600,19 +523,8 @@ def hisa_token_weights(q_att: torch.Tensor, k_att: torch.Tensor, topk_idx: torch
                        scale: float, weights: torch.Tensor, stream=None) -> torch.Tensor:
     """Add the attention weight of every selected token of the bf16 cache, summed over the
     heads, to weights int64 [rows] (units of HISA_WEIGHT_UNIT); returns weights."""
-    dev, i32 = _device_of(q_att, "q_att"), torch.int32
-    q = _at(q_att, "q_att", torch.bfloat16, dev)
-    ka = _at(k_att, "k_att", torch.bfloat16, dev, HISA_ATT_DIM)
-    idx = _at(topk_idx, "topk_idx", i32, dev)
-    cq = _at(cu_seqlens_q, "cu_seqlens_q", i32, dev)
-    ck = _at(cu_seqlens_k, "cu_seqlens_k", i32, dev)
-    ls = _at(lse, "lse", torch.float32, dev)
-    w = _at(weights, "weights", torch.int64, dev)
-    total_q, heads, k = _att_shapes(q_att, topk_idx, lse, weights, k_att.shape[0])
-    S = _seqs(cu_seqlens_q, cu_seqlens_k, None)
-    _check(lib().hisa_token_weights(q, ka, idx, ls, cq, ck, S, total_q, heads, k, float(scale),
-                                    w, _raw_stream(stream, dev)), "hisa_token_weights")
-    return weights
+    return _native().token_weights(q_att, k_att, topk_idx, lse, cu_seqlens_q, cu_seqlens_k, scale,
+                                   weights, None if stream is None else stream.cuda_stream)
 
 
 def hisa_evict_select(weights: torch.Tensor, cu_seqlens_k: torch.Tensor,
@@ -621,71 +533,13 @@ def hisa_evict_select(weights: torch.Tensor, cu_seqlens_k: torch.Tensor,
                       kept_len: Optional[torch.Tensor] = None, stream=None):
     """Which tokens of every sequence stay: the first n_sink, the last n_recent and those of
     the largest weights, keep[s] in all; returns (kept int32 [rows], kept_len int32 [S])."""
-    dev, i32 = _device_of(weights, "weights"), torch.int32
-    w = _at(weights, "weights", torch.int64, dev)
-    ck = _at(cu_seqlens_k, "cu_seqlens_k", i32, dev)
-    n = None if seqlens_k is None else _at(seqlens_k, "seqlens_k", i32, dev)
-    b = _at(keep, "keep", i32, dev)
-    S, rows = _seqs(None, cu_seqlens_k, seqlens_k), weights.numel()
-    if keep.numel() != S:
-        raise ValueError("keep must hold one budget per sequence")
-    if kept is None:
-        kept = torch.empty(rows, dtype=i32, device=weights.device)
-    if kept_len is None:
-        kept_len = torch.empty(S, dtype=i32, device=weights.device)
-    ks, kn = _at(kept, "kept", i32, dev), _at(kept_len, "kept_len", i32, dev)
-    if kept.numel() != rows or kept_len.numel() != S:
-        raise ValueError("kept must hold one number per cache row, kept_len one per sequence")
-    _check(lib().hisa_evict_select(w, ck, n, b, S, int(max_seqlen_k), int(n_sink), int(n_recent),
-                                   ks, kn, _raw_stream(stream, dev)), "hisa_evict_select")
-    return kept, kept_len
-
-
-class _Rows(ctypes.Structure):
-    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p),
-                ("row_bytes", ctypes.c_size_t)]
+    return _native().evict_select(weights, cu_seqlens_k, seqlens_k, keep, max_seqlen_k, n_sink,
+                                  n_recent, kept, kept_len, None if stream is None else stream.cuda_stream)
 
 
 def hisa_evict_rows(src, dst, cu_src: torch.Tensor, cu_dst: torch.Tensor, kept: torch.Tensor,
                     kept_len: torch.Tensor, max_keep: int, stream=None) -> None:
     """Move the rows that stay (kept, kept_len of hisa_evict_select) of the row arrays src to
     the front of their regions of the arrays dst; the same tensor in both moves in place."""
-    if len(src) != len(dst) or len(src) > HISA_MAX_ROW_ARRAYS:
-        raise ValueError(f"src and dst must be as many arrays, at most {HISA_MAX_ROW_ARRAYS}")
-    dev, i32 = _device_of(kept, "kept"), torch.int32
-    ks, kn = _at(kept, "kept", i32, dev), _at(kept_len, "kept_len", i32, dev)
-    cs, cd = _at(cu_src, "cu_src", i32, dev), _at(cu_dst, "cu_dst", i32, dev)
-    S, n_rows = _seqs(cu_dst, cu_src, kept_len), kept.numel()
-    rows = []  # source, destination and bytes of a row, as the C structure has them
-    # first byte, last byte behind, whether a destination; in place counts once
-    spans = [(ks, ks + 4 * n_rows, False), (kn, kn + 4 * S, False)]
-    for a, b in zip(src, dst):
-        dt = a.dtype
-        pa = _at(a, "a source", dt, dev)
-        pb = pa if b is a else _at(b, "a destination", b.dtype, dev)
-        sa, sb, na, nb = a.shape, b.shape, a.numel(), b.numel()
-        if not sa or not sb or b.dtype is not dt:
-            raise ValueError("a source and its destination must have rows of one type and shape")
-        if sa[0] != n_rows:
-            raise ValueError("kept must hold one number per source row")
-        width = na // n_rows if n_rows else 1
-        if width * sb[0] != nb:
-            raise ValueError("a source and its destination must have rows of one type and shape")
-        size = dt.itemsize
-        rows += (pa, pb, width * size)
-        spans.append((pb, pb + nb * size, True))
-        if pa != pb or na != nb:
-            spans.append((pa, pa + na * size, False))
-    # in order of their starts, a span may touch none before it, unless both are sources
-    spans.sort()
-    end = end_dst = 0
-    for a, b, is_dst in spans:
-        if a < (end if is_dst else end_dst) and a < b:
-            raise ValueError("a destination overlaps a source or kept, or two destinations overlap")
-        if b > end:
-            end = b
-        if is_dst and b > end_dst:
-            end_dst = b
-    rows = struct.pack(f"{len(rows)}Q", *rows)
-    _check(lib().hisa_evict_rows(rows, len(src), cs, cd, ks, kn, S, int(max_keep),
-                                 _raw_stream(stream, dev)), "hisa_evict_rows")
+    _native().evict_rows(src, dst, cu_src, cu_dst, kept, kept_len, max_keep,
+                         None if stream is None else stream.cuda_stream)

@@ -3,7 +3,8 @@
 Each .cu file under csrc/ is compiled by nvcc into an object with
 ``-gencode arch=compute_100a,code=sm_100a -O3 -lineinfo`` and the objects are
 linked into ``sparse_attention_top_hisa_b200/libhisa.so`` (CUDA runtime linked
-statically).  Run ``python -m sparse_attention_top_hisa_b200.build``.
+statically).  csrc/torch_binding.cpp is compiled by g++ against the installed torch
+into ``_hisa_torch.so``.  Run ``python -m sparse_attention_top_hisa_b200.build``.
 """
 
 from __future__ import annotations
@@ -13,12 +14,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhisa.so")
+BINDING = os.path.join(HERE, "_hisa_torch.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -34,7 +37,7 @@ def sources():
 
 
 def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".cpp")]
     files.append(os.path.join(ROOT, "include", "hisa.h"))
     return files
 
@@ -51,8 +54,34 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile the argument checks of the per-step entry points; returns the module's path."""
+    src, header = os.path.join(CSRC, "torch_binding.cpp"), os.path.join(ROOT, "include", "hisa.h")
+    newest = max(os.path.getmtime(f) for f in (src, header))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    import torch
+    base = os.path.dirname(torch.__file__)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    inc = [os.path.join(ROOT, "include"), os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"],
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in inc), src, "-o", tmp, "-L" + os.path.join(base, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile every kernel source and link libhisa.so; returns its path."""
+    """Compile every kernel source and link libhisa.so, and the binding; returns the
+    library's path."""
+    build_binding(force)
     srcs = sources()
     newest = max(os.path.getmtime(f) for f in _deps())
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
