@@ -7,9 +7,9 @@
 // over the entries j >= 0 of the index row.  One warp takes 32 selected tokens at a time
 // and does everything to them: it copies their rows (144 bytes each) into a ring of its
 // own, turns the key nibbles into fp16 fragments, multiplies, keeps the running maximum
-// and sum of its share, turns the value nibbles into fragments and multiplies again.  No
-// warp waits for another until its share is done; then the warps of a CTA, and the CTAs
-// of a row's cluster, are merged by their maxima and sums.
+// and sum of its share, turns the value nibbles into fragments and multiplies again.  With
+// many rows a warp has a row to itself; with few, the warps of a CTA and the CTAs of a
+// cluster share one and are merged by their maxima and sums.
 //
 // The fragments' dimensions are assigned so that no value moves between lanes.  With
 // g = lane / 4 and c = lane % 4, in m16n8k16:
@@ -25,7 +25,7 @@
 // Precision: q (bf16) is held as fp16 times a power of two per head, exact over 29 binades
 // below the head's largest value; the products are exact and summed in fp32; maxima and
 // sums are fp32; the softmax weights enter the value product as fp16 (relative error at
-// most 2^-12, an eighth of the bf16 output's own rounding), taken against a reference that
+// most 2^-11, an eighth of the bf16 output's own rounding), taken against a reference that
 // the maximum never exceeds by more than 2^8.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -60,6 +60,17 @@ static_assert(16 * A4_OSTRIDE * 4 <= a4_ring(1) && 32 * A4_OSTRIDE * 4 <= a4_rin
 __device__ __forceinline__ int a4_chunk(int t, int chunk) {
   return chunk ^ (((t >> 1) & 3) << 1) ^ ((t & 1) << 2);
 }
+
+// What bounds it: issue.  A step of 32 tokens and 16 heads takes about 650 instructions
+// beside its 64 matrix instructions (352 of them turn 8192 nibbles into fp16), which in
+// this mix leave room for about 2.5 instructions per cycle; the gather (160 bytes of L2
+// sectors per token, 4.9 TB/s of the 17 the same copies reach alone) and DRAM are idle
+// beside it.  8192 queries x 2048 tokens x 16 heads: 550 us, 250 TFLOP/s.  Measured and
+// left out: the value product of one step written between the scores of the next (658
+// against 637 us at the time), four CTAs per SM of 128 registers (697, spills), and the
+// same products on the tensor core that reads shared memory: it takes about 85 cycles for
+// each 128 tokens x 16 dimensions whatever the number of heads up to 32, so the scores alone
+// would cost 170 cycles of a step's 290.
 
 // 16 bytes global -> shared; zeros when !ok
 __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *src, bool ok) {
@@ -254,8 +265,7 @@ __device__ __forceinline__ void kv4_values(const ValueRaw &r, int i, int b,
 }
 
 // A warp's walk over its steps: the token ids are read one step ahead of the copies, the
-// copies run AHEAD steps ahead of the products, over NST stages: the NST - 1 - AHEAD steps
-// before the current one stay readable.
+// copies run AHEAD = NST - 1 steps ahead of the products, over NST stages.
 // VALUES: the value halves of the rows are copied too.
 template <int NST, int AHEAD, bool VALUES>
 struct Ring {
@@ -334,8 +344,7 @@ struct Ring {
     for (int n = 0; n < AHEAD; n++) mask[n] = copy(lp, lane);
   }
   // start one more copy, wait for the next step; its stage and the mask of its valid tokens
-  __device__ __forceinline__ uint32_t arrive(const LanePlaces &lp, int lane,
-                                                   uint32_t &valid) {
+  __device__ __forceinline__ uint32_t arrive(const LanePlaces &lp, int lane, uint32_t &valid) {
     __syncwarp();  // every lane has read the stage that is filled now
     const uint32_t more = copy(lp, lane);
     valid = mask[0];

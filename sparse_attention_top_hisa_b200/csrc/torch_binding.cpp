@@ -4,10 +4,12 @@
 // torch tensors positionally, check device, type, contiguity and shape, pass addresses and
 // the stream to the C ABI and hand any status but HISA_OK to the callable that raises
 // HisaError.  The entry points' addresses come from the loaded library (setup()).
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <algorithm>
@@ -48,7 +50,7 @@ struct Args {
     if (!x.is_cuda()) bad("%s must be a CUDA tensor", name);
     if (x.scalar_type() != t) bad("%s must be %s", name, c10::toString(t));
     if (!x.is_contiguous()) bad("%s must be contiguous", name);
-    if (cols >= 0 && (x.dim() != 2 || x.size(1) != cols)) bad("%s has another shape than [*, width]", name);
+    if (cols >= 0 && (x.dim() != 2 || x.size(1) != cols)) bad(cols == HISA_ATT_DIM ? "%s must have shape [*, 128]" : "%s must have shape [*, 16]", name);
     place(x, name);
     return x;
   }
@@ -71,11 +73,30 @@ struct Args {
     if (v < INT32_MIN || v > INT32_MAX) bad("a size does not fit 32 bits");
     return (int)v;
   }
-  void on(int i) {  // the stream: None is the current one
-    stream = none(i) ? (void *)c10::cuda::getCurrentCUDAStream(dev).stream()
-                     : PyLong_AsVoidPtr(a[i]);
+  bool given = false;  // the caller named a stream
+  void on(int i) {     // the stream: None is the current one
+    given = !none(i);
+    stream = given ? PyLong_AsVoidPtr(a[i]) : (void *)c10::cuda::getCurrentCUDAStream(dev).stream();
     if (PyErr_Occurred()) throw Bad();
   }
+  // A new tensor whose memory belongs to the call's stream: freed, it is not handed to
+  // another stream's work while the call may still write it.
+  at::Tensor fresh(at::IntArrayRef sizes, const at::TensorOptions &o) const {
+    if (!given) return at::empty(sizes, o);
+    c10::cuda::CUDAStreamGuard guard(
+        c10::cuda::getStreamFromExternal((cudaStream_t)stream, (c10::DeviceIndex)dev));
+    return at::empty(sizes, o);
+  }
+};
+
+struct Items {  // of a Python sequence, held while they are looked at
+  PyObject *s;
+  explicit Items(PyObject *o) : s(PySequence_Fast(o, "src and dst must be sequences")) {
+    if (!s) throw Bad();
+  }
+  ~Items() { Py_DECREF(s); }
+  Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(s); }
+  PyObject *operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(s, i); }
 };
 
 template <typename T>
@@ -144,14 +165,14 @@ PyObject *kv4_load(Args g) {
   const int s = sequences(&cq, ck, lens);
   if (total_q < 0) bad("total_q must not be negative");
   at::Tensor out[2];
+  g.on(8);
   for (int i = 0; i < 2; i++) {
     if (g.none(6 + i))
-      out[i] = at::empty({total_q, HISA_ATT_DIM}, kv4->options().dtype(at::kBFloat16));
+      out[i] = g.fresh({total_q, HISA_ATT_DIM}, kv4->options().dtype(at::kBFloat16));
     else
       out[i] = g.tensor(6 + i, i ? "v_out" : "k_out", at::kBFloat16, HISA_ATT_DIM);
     if (out[i].size(0) != total_q) bad("k_out and v_out need one row per query row");
   }
-  g.on(8);
   check(p_load(at_of<uint8_t>(*kv4), at_of<uint8_t>(*scale), at_of<int32_t>(cq),
                at_of<int32_t>(ck), n, s, total_q, at_of<hisa_bf16>(out[0]),
                at_of<hisa_bf16>(out[1]), g.stream),
@@ -193,18 +214,18 @@ PyObject *attention_kv4(Args g) {
   const AttShape s = att_shape(q, idx, lse, w, kv4->size(0));
   const int seqs = sequences(&cq, ck, nullptr);
   if (w && !lse) bad("weights need lse");
-  at::Tensor fresh;
-  if (g.none(7)) fresh = at::empty_like(q);
-  const at::Tensor &out = g.none(7) ? fresh : g.tensor(7, "out", at::kBFloat16);
-  if (out.sizes() != q.sizes()) bad("out must have the shape of q_att");
   g.on(10);
+  at::Tensor made;
+  if (g.none(7)) made = g.fresh(q.sizes(), q.options());
+  const at::Tensor &out = g.none(7) ? made : g.tensor(7, "out", at::kBFloat16);
+  if (out.sizes() != q.sizes()) bad("out must have the shape of q_att");
   check(p_attention(at_of<hisa_bf16>(q), at_of<uint8_t>(*kv4), at_of<uint8_t>(*scale),
                     at_of<int32_t>(idx), at_of<int32_t>(cq), at_of<int32_t>(ck), seqs, s.total_q,
                     s.heads, s.k, (float)sc, at_of<hisa_bf16>(out),
                     lse ? at_of<float>(*lse) : nullptr, w ? at_of<int64_t>(*w) : nullptr,
                     g.stream),
         "hisa_sparse_attention_kv4");
-  if (g.none(7)) return THPVariable_Wrap(fresh);
+  if (g.none(7)) return THPVariable_Wrap(made);
   Py_INCREF(g.a[7]);
   return g.a[7];
 }
@@ -242,11 +263,11 @@ PyObject *evict_select(Args g) {
   if (keep.numel() != s) bad("keep must hold one budget per sequence");
   at::Tensor kept, kept_len;
   const auto i32 = w.options().dtype(at::kInt);
-  kept = g.none(7) ? at::empty({w.numel()}, i32) : g.tensor(7, "kept", at::kInt);
-  kept_len = g.none(8) ? at::empty({s}, i32) : g.tensor(8, "kept_len", at::kInt);
+  g.on(9);
+  kept = g.none(7) ? g.fresh({w.numel()}, i32) : g.tensor(7, "kept", at::kInt);
+  kept_len = g.none(8) ? g.fresh({s}, i32) : g.tensor(8, "kept_len", at::kInt);
   if (kept.numel() != w.numel() || kept_len.numel() != s)
     bad("kept must hold one number per cache row, kept_len one per sequence");
-  g.on(9);
   check(p_select(at_of<int64_t>(w), at_of<int32_t>(ck), n, at_of<int32_t>(keep), s, g.whole(4),
                  g.whole(5), g.whole(6), at_of<int32_t>(kept), at_of<int32_t>(kept_len),
                  g.stream),
@@ -270,12 +291,9 @@ PyObject *evict_rows(Args g) {
   const at::Tensor &cs = g.tensor(2, "cu_src", at::kInt);
   const at::Tensor &cd = g.tensor(3, "cu_dst", at::kInt);
   const int s = sequences(&cd, cs, &kept_len);
-  const Py_ssize_t n = PySequence_Size(g.a[0]);
-  if (n < 0 || PyErr_Occurred()) throw Bad();
-  if (PySequence_Size(g.a[1]) != n || n > HISA_MAX_ROW_ARRAYS) {
-    if (PyErr_Occurred()) throw Bad();
-    bad("src and dst must be as many arrays, at most 8");
-  }
+  const Items src(g.a[0]), dst(g.a[1]);
+  const Py_ssize_t n = src.size();
+  if (dst.size() != n || n > HISA_MAX_ROW_ARRAYS) bad("src and dst must be as many arrays, at most 8");
   std::vector<Span> spans;
   hisa_rows rows[HISA_MAX_ROW_ARRAYS];
   auto span = [&](const at::Tensor &x, bool dst) {
@@ -287,9 +305,7 @@ PyObject *evict_rows(Args g) {
   for (Py_ssize_t i = 0; i < n; i++) {
     const at::Tensor *t[2];
     for (int d = 0; d < 2; d++) {
-      PyObject *o = PySequence_GetItem(g.a[d], i);
-      if (!o) throw Bad();
-      Py_DECREF(o);  // the sequence holds it
+      PyObject *o = d ? dst[i] : src[i];
       const char *name = d ? "a destination" : "a source";
       if (!THPVariable_Check(o)) bad("%s must be a tensor", name);
       t[d] = &THPVariable_Unpack(o);
@@ -330,15 +346,15 @@ PyObject *entry(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PyErr_Format(PyExc_TypeError, "%d arguments are wanted, got %zd", N, n);
     return nullptr;
   }
+  HANDLE_TH_ERRORS
   try {
     Args g;
     g.a = a;
     return F(g);
   } catch (const Bad &) {
-  } catch (const std::exception &e) {  // of torch
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
   }
-  return nullptr;
+  END_HANDLE_TH_ERRORS
 }
 
 // raise, then the addresses of the six entry points in the order of the pointers above
