@@ -389,6 +389,7 @@ struct RowArrays {
   uint8_t *dst[HISA_MAX_ROW_ARRAYS];
   int bytes[HISA_MAX_ROW_ARRAYS];  // of a row
   int vec[HISA_MAX_ROW_ARRAYS];    // of a copied piece: 16, 8 or 4
+  int shift[HISA_MAX_ROW_ARRAYS];  // log2 of a row's pieces, -1 where that is no whole number
   int n;
 };
 
@@ -424,8 +425,8 @@ __device__ __forceinline__ EvictSeq evict_seq(const int32_t *cu_src, const int32
 // Rows rows[0 .. n) of the source to drow, drow + 1, ...: ER_UNROLL pieces of a thread are
 // read before any is written.
 template <typename T>
-__device__ __forceinline__ void move_rows(const uint8_t *src, uint8_t *dst, int per, const int *rows,
-                                          int n, size_t sbase, size_t drow) {
+__device__ __forceinline__ void move_rows(const uint8_t *src, uint8_t *dst, int per, int shift,
+                                          const int *rows, int n, size_t sbase, size_t drow) {
   const T *s = reinterpret_cast<const T *>(src) + sbase * per;
   T *d = reinterpret_cast<T *>(dst) + drow * per;
   const int total = n * per;
@@ -437,7 +438,7 @@ __device__ __forceinline__ void move_rows(const uint8_t *src, uint8_t *dst, int 
       const int x = x0 + u * ER_THREADS;
       ok[u] = false;
       if (x < total) {
-        const int r = x / per, from = rows[r];
+        const int r = shift >= 0 ? x >> shift : x / per, from = rows[r];
         ok[u] = from >= 0;
         if (ok[u]) v[u] = __ldg(s + (size_t)from * per + (x - r * per));
       }
@@ -467,11 +468,11 @@ evict_rows_kernel(const __grid_constant__ RowArrays a, const int32_t *__restrict
   for (int k = 0; k < a.n; k++) {
     const size_t sb = (size_t)q.sbase, d = (size_t)q.dbase + r0;
     if (a.vec[k] == 16)
-      move_rows<uint4>(a.src[k], a.dst[k], a.bytes[k] / 16, rows, n, sb, d);
+      move_rows<uint4>(a.src[k], a.dst[k], a.bytes[k] / 16, a.shift[k], rows, n, sb, d);
     else if (a.vec[k] == 8)
-      move_rows<uint2>(a.src[k], a.dst[k], a.bytes[k] / 8, rows, n, sb, d);
+      move_rows<uint2>(a.src[k], a.dst[k], a.bytes[k] / 8, a.shift[k], rows, n, sb, d);
     else
-      move_rows<uint32_t>(a.src[k], a.dst[k], a.bytes[k] / 4, rows, n, sb, d);
+      move_rows<uint32_t>(a.src[k], a.dst[k], a.bytes[k] / 4, a.shift[k], rows, n, sb, d);
   }
 }
 
@@ -568,6 +569,7 @@ cudaError_t launch_evict_rows(const hisa_rows *arrays, int n, const int32_t *cu_
     a.dst[a.n] = static_cast<uint8_t *>(arrays[i].dst);
     a.bytes[a.n] = (int)arrays[i].row_bytes;
     a.vec[a.n] = v;
+    a.shift[a.n] = (per & (per - 1)) == 0 ? __builtin_ctz((unsigned)per) : -1;
     a.n++;
     if (&a == &in) columns += v == 16 && per % 2 == 0 ? per / 2 : per;
   }

@@ -5,11 +5,11 @@
 //   even, clamped to -7..7.
 // Every decision is the exact one.  a and x have 8 significant bits, and a tie of a / 7
 // lies at 7 * (a 5-bit number) and one of x / s at s * (a 4-bit number): both are 8-bit
-// numbers, so a quotient that is not a tie is at least 2^-8 (relative) from one, and the
-// correctly rounded fp32 quotient falls on the right side.  For x / s the product with
-// the rounded reciprocal of s is taken instead and rounded to a multiple of 2^-12 first
-// (in the FMA that adds 3072), which puts ties back where they belong and moves nothing
-// else across one; a second sum rounds to a whole number.
+// numbers, so a quotient that is not a tie is at least 2^-8 (relative) from one.  The
+// products with the rounded reciprocals of 7 and s are off by a few 2^-23; rounding them
+// to 12 bits (a / 7) and to a multiple of 2^-12 (x / s, in the FMA that adds 3072) puts
+// ties back where they belong and moves nothing else across one, and a second rounding
+// decides.
 //
 // A sequence whose region or length does not fit, or with fewer live tokens than query
 // rows, is skipped whole.
@@ -27,17 +27,36 @@ namespace hisa {
 
 constexpr int KVS_THREADS = 128, KVS_WARPS = KVS_THREADS / 32;
 
-// e5m3 byte of t >= 0 (finite), rounded to nearest even, at most 896 (byte 198)
-__device__ __forceinline__ uint32_t e5m3_round(float t) {
-  uint32_t b;
-  if (t < 0x1p-14f) {
-    b = (uint32_t)__float2int_rn(t * 0x1p17f);  // multiples of 2^-17; 8 is 2^-14
-  } else {
-    uint32_t u = __float_as_uint(t);
-    u += 0x7FFFFu + ((u >> 20) & 1u);
-    b = (u >> 20) - ((127u - 15u) << 3);
+// e5m3 byte of amax / 7 (amax >= 0, finite, bf16), rounded to nearest even, at most 896
+// (byte 198)
+__device__ __forceinline__ uint32_t e5m3_seventh(float amax) {
+  // 12 significant bits: ties of the quotient are exact again
+  const uint32_t u = (__float_as_uint(amax * (1.f / 7.f)) + 0x800u) & 0xFFFFF000u;
+  const float t = __uint_as_float(u);
+  const uint32_t normal = ((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - ((127u - 15u) << 3);
+  const uint32_t tiny = (uint32_t)__float2int_rn(t * 0x1p17f);  // multiples of 2^-17; 8 is 2^-14
+  return min(t < 0x1p-14f ? tiny : normal, 198u);
+}
+
+__device__ __forceinline__ float reciprocal(float s) {  // of a normal s, off by an ulp or two
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
+// Eight values (pairs of bf16) times r as nibbles q + 8; CLAMP: q may pass 7.
+template <bool CLAMP>
+__device__ __forceinline__ uint32_t nibbles(const uint32_t *w, float r) {
+  uint32_t sum = 0;
+#pragma unroll
+  for (int j = 7; j >= 0; j--) {
+    float t = fmaf((j & 1) ? bf_hi(w[j >> 1]) : bf_lo(w[j >> 1]), r, 3072.f);
+    if (CLAMP) t = fminf(fmaxf(t, 3065.f), 3079.f);
+    // 1.5 * 2^23 + 8 + q: rounds to a whole number, whose bits are a constant and q + 8
+    t += 12582912.f + 8.f - 3072.f;
+    sum = sum * 16u + __float_as_uint(t);
   }
-  return min(b, 198u);
+  return sum - 0x11111111u * 0x4B400000u;
 }
 
 __device__ __forceinline__ float e5m3_value(uint32_t b) {
@@ -51,31 +70,35 @@ __device__ __forceinline__ void cache_rows(const int32_t *cu_q, const int32_t *c
                                            const int32_t *seqlens, int S, int row, int total_q,
                                            int *status, long long (&at)[R]) {
   const int lane = threadIdx.x & 31, first = __shfl_sync(0xffffffffu, row, 0);
-  int s = 0, q0 = 0, q1 = 0, k0 = 0, cap = 0, len = 0;
+  int q0 = 0, q1 = 0;
+  long long base = -1;  // the cache row of query row q0, -1: the sequence is skipped
+  auto look = [&](int r) {
+    const int s = find_seq_warp(cu_q, S, r, lane);
+    q0 = __ldg(cu_q + s);
+    q1 = __ldg(cu_q + s + 1);
+    const int k0 = __ldg(cu_k + s), cap = __ldg(cu_k + s + 1) - k0;
+    const int len = seqlens ? __ldg(seqlens + s) : cap;
+    base = (long long)k0 + len - (q1 - q0);
+    if (k0 % BLK != 0) {
+      raise_status(status, HISA_ERR_UNALIGNED);
+      base = -1;
+    } else if (len < 0 || len > cap || len < q1 - q0 || r < q0 || r >= q1) {
+      raise_status(status, HISA_ERR_INVALID_ARG);
+      base = -1;
+      q1 = r + 1;  // the next row looks for itself
+    }
+  };
+  look(min(first, total_q - 1));
+  if (first + 2 * R <= q1 && first + 2 * R <= total_q) {  // all of one sequence
+#pragma unroll
+    for (int i = 0; i < R; i++) at[i] = base < 0 ? -1 : base + (row + 2 * i - q0);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 2 * R; i++) {  // the warp's rows in order
     const int r = first + i;
-    if (r >= total_q) {
-      if (lane / 16 == i % 2) at[i / 2] = -1;
-      continue;
-    }
-    if (i == 0 || r >= q1) {
-      s = find_seq_warp(cu_q, S, r, lane);
-      q0 = __ldg(cu_q + s);
-      q1 = __ldg(cu_q + s + 1);
-      k0 = __ldg(cu_k + s);
-      cap = __ldg(cu_k + s + 1) - k0;
-      len = seqlens ? __ldg(seqlens + s) : cap;
-    }
-    bool ok = true;
-    if (k0 % BLK != 0) {
-      raise_status(status, HISA_ERR_UNALIGNED);
-      ok = false;
-    } else if (len < 0 || len > cap || len < q1 - q0 || r < q0 || r >= q1) {
-      raise_status(status, HISA_ERR_INVALID_ARG);
-      ok = false;
-    }
-    if (lane / 16 == i % 2) at[i / 2] = ok ? (long long)k0 + (len - (q1 - q0) + (r - q0)) : -1;
+    if (r < total_q && r >= q1) look(r);
+    if (lane / 16 == i % 2) at[i / 2] = r < total_q && base >= 0 ? base + (r - q0) : -1;
   }
 }
 
@@ -114,24 +137,16 @@ kv4_store_kernel(const uint16_t *__restrict__ k_new, const uint16_t *__restrict_
       byte = 255u;
       raise_status(status, HISA_ERR_INVALID_ARG);
     } else {
-      byte = e5m3_round(__fdiv_rn(__uint_as_float(mx << 16), 7.f));
+      byte = e5m3_seventh(__uint_as_float(mx << 16));
       const float s = e5m3_value(byte);
-      const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+      const float r = s > 0.f ? reciprocal(s) : 0.f;
       // |x / s| < 7.5 by the choice of s, but for the largest and the subnormal scales
-      const bool clamp = byte < 8u || byte == 198u;
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        uint32_t sum = 0;
-#pragma unroll
-        for (int j = 7; j >= 0; j--) {
-          const uint32_t x2 = w[4 * h + (j >> 1)];
-          float t = fmaf((j & 1) ? bf_hi(x2) : bf_lo(x2), r, 3072.f);  // multiples of 2^-12
-          if (clamp) t = fminf(fmaxf(t, 3065.f), 3079.f);
-          // 1.5 * 2^23 + 8 + q: rounds to a whole number, whose bits are a constant and q + 8
-          t += 12582912.f + 8.f - 3072.f;
-          sum = sum * 16u + __float_as_uint(t);
-        }
-        c[h] = sum - 0x11111111u * 0x4B400000u;
+      if (byte < 8u || byte == 198u) {
+        c[0] = nibbles<true>(w, r);
+        c[1] = nibbles<true>(w + 4, r);
+      } else {
+        c[0] = nibbles<false>(w, r);
+        c[1] = nibbles<false>(w + 4, r);
       }
     }
     *reinterpret_cast<uint2 *>(kv4 + (size_t)dst[i] * KV4_ROW + g * 8) = make_uint2(c[0], c[1]);
