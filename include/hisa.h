@@ -387,8 +387,10 @@ hisa_status hisa_kv4_load(const uint8_t *kv4, const uint8_t *kv4_scale,
  *                  result independent of the order of the additions.  Not cleared here.  A
  *                  weight that is not a number adds nothing and raises
  *                  HISA_ERR_INVALID_ARG in the device status word.
- * Every other argument and the errors are those of hisa_sparse_attention.  out must be
- * 16-byte aligned.
+ * Every other argument and the errors are those of hisa_sparse_attention, and total_q is
+ * below 2^25 and k at most 2^28.  out must be 16-byte aligned.  A query row behind the last
+ * sequence (cu_seqlens_q[num_seqs] <= row < total_q, in a padded batch) has no tokens: an
+ * index >= 0 in it is one outside the region.
  * Precision: q.k are sums of exact products in fp32 (a value of q more than 2^28 times
  * smaller than its head's largest loses bits); maxima, sums, lse and weights are fp32;
  * the softmax weights enter the value product as fp16 (11 significant bits) and the
@@ -408,7 +410,8 @@ hisa_status hisa_sparse_attention_kv4(const hisa_bf16 *q_att, const uint8_t *kv4
  * over the entries j >= 0 of topk_idx[i], rounded to units of 2^-32 as above.
  *   lse            fp32 [total_q, num_heads] as hisa_sparse_attention wrote it for the same
  *                  q_att, k_att, topk_idx and scale; a head with lse -inf adds nothing.
- * Any subset of the query rows may be given (an observation window at a prompt's end).
+ * Any subset of the query rows may be given (an observation window at a prompt's end);
+ * rows behind the last sequence and the limits of total_q and k as above.
  * A weight that is not a number, or larger than 4096, adds nothing and raises
  * HISA_ERR_INVALID_ARG in the device status word, as does an index outside the region.
  */
@@ -433,7 +436,8 @@ hisa_status hisa_token_weights(const hisa_bf16 *q_att, const hisa_bf16 *k_att,
  *                  as they were.
  *   kept_len (out) int32 [num_seqs]: the count, min(len_s, keep[s]).
  * max_seqlen_k is at most 2^30.  A sequence with a negative budget, or with a length
- * outside its region or above max_seqlen_k, gets kept_len -1 and raises HISA_ERR_INVALID_ARG in the device status word.
+ * outside its region or above max_seqlen_k, gets kept_len -1 and raises
+ * HISA_ERR_INVALID_ARG in the device status word.
  */
 hisa_status hisa_evict_select(const int64_t *weights, const int32_t *cu_seqlens_k,
                               const int32_t *seqlens_k, const int32_t *keep, int num_seqs,
@@ -455,7 +459,7 @@ hisa_status hisa_evict_select(const int64_t *weights, const int32_t *cu_seqlens_
  *                  for arrays moved in place.
  *   kept, kept_len as hisa_evict_select wrote them (kept strictly ascending per sequence);
  *                  neither may be among the arrays.
- *   max_keep       >= every kept_len (host copy, sizes the grid).
+ *   max_keep       >= every kept_len (host copy, sizes the grid); 0 launches nothing.
  * Rows past kept_len[s] of a destination region are left as they were.  Afterwards
  * kept_len is the new seqlens_k (with cu_dst as cu_seqlens_k), and hisa_pool_blocks renews
  * the representatives.  Reported in the device status word: a kept_len that is negative,

@@ -558,8 +558,8 @@ hisa_status hisa_sparse_attention_kv4(const hisa_bf16 *q_att, const uint8_t *kv4
                                       int num_seqs, int total_q, int num_heads, int k,
                                       float scale, hisa_bf16 *out, float *lse, int64_t *weights,
                                       hisa_stream_t stream) {
-  if (num_heads < 1 || num_heads > HISA_ATT_MAX_HEADS || k < 1 || num_seqs < 0 || total_q < 0 ||
-      !(scale == scale))
+  if (num_heads < 1 || num_heads > HISA_ATT_MAX_HEADS || k < 1 || k > (1 << 28) || num_seqs < 0 ||
+      total_q < 0 || !(scale == scale))
     return HISA_ERR_INVALID_ARG;
   if (total_q == 0) return HISA_OK;
   if (num_seqs == 0 || total_q >= (1 << 25)) return HISA_ERR_INVALID_ARG;
@@ -583,8 +583,8 @@ hisa_status hisa_token_weights(const hisa_bf16 *q_att, const hisa_bf16 *k_att,
                                const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
                                int num_seqs, int total_q, int num_heads, int k, float scale,
                                int64_t *weights, hisa_stream_t stream) {
-  if (num_heads < 1 || num_heads > HISA_ATT_MAX_HEADS || k < 1 || num_seqs < 0 || total_q < 0 ||
-      !(scale == scale))
+  if (num_heads < 1 || num_heads > HISA_ATT_MAX_HEADS || k < 1 || k > (1 << 28) || num_seqs < 0 ||
+      total_q < 0 || !(scale == scale))
     return HISA_ERR_INVALID_ARG;
   if (total_q == 0) return HISA_OK;
   if (num_seqs == 0 || total_q >= (1 << 25)) return HISA_ERR_INVALID_ARG;

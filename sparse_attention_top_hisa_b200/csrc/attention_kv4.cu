@@ -679,8 +679,8 @@ attn_kv4_rows_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict__
   uint4 *qs = reinterpret_cast<uint4 *>(a4_smem + A4_WARPS * RING + warp * MT * 4096);
   uint8_t *mem = a4_smem + warp * RING;
 
-  const int s = find_seq_warp(cu_q, S, row, lane);
-  const int kbase = __ldg(cu_k + s), kcap = __ldg(cu_k + s + 1) - kbase;
+  const Region rg = region_of(cu_q, cu_k, S, row, lane);
+  const int kbase = rg.base, kcap = rg.tokens;
   const LanePlaces lp(lane);
   const int32_t *irow = idx + (size_t)row * topk;
   Ring<NST, NST - 1, true> ring;
@@ -764,8 +764,8 @@ attn_kv4_split_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict_
   float *wl = wm + A4_WARPS * NH;                                     // [warps][NH]
   float *cm = wl + A4_WARPS * NH, *cs = cm + NH;  // the CTA's maximum and sum per head
   float *xm = cs + NH;                            // factors of the cluster's CTAs [NH][C]
-  const int s = find_seq_warp(cu_q, S, row, lane);
-  const int kbase = __ldg(cu_k + s), kcap = __ldg(cu_k + s + 1) - kbase;
+  const Region rg = region_of(cu_q, cu_k, S, row, lane);
+  const int kbase = rg.base, kcap = rg.tokens;
   const LanePlaces lp(lane);
   const int e0 = me * per_cta, e1 = min(topk, e0 + per_cta);
   const int32_t *irow = idx + (size_t)row * topk;
@@ -1028,8 +1028,8 @@ token_weights_kernel(const uint16_t *__restrict__ q, const uint16_t *__restrict_
   const int row = (int)(item / parts);
   if (row >= total_q) return;  // the whole warp; the others do not wait for it
   const int g = lane >> 2, c = lane & 3;
-  const int s = find_seq_warp(cu_q, S, row, lane);
-  const int kbase = __ldg(cu_k + s), kcap = __ldg(cu_k + s + 1) - kbase;
+  const Region rg = region_of(cu_q, cu_k, S, row, lane);
+  const int kbase = rg.base, kcap = rg.tokens;
   const int32_t *irow = idx + (size_t)row * topk;
   const int steps = (topk + A4_STEP - 1) / A4_STEP;
   const int first = (int)(item - (long long)row * parts), stride = parts;

@@ -575,7 +575,7 @@ cudaError_t launch_evict_rows(const hisa_rows *arrays, int n, const int32_t *cu_
   }
   if (out.n > 0) {
     ProfScope ps(K_EVICT_ROWS, st);
-    evict_rows_kernel<<<dim3((max_keep + ER_ROWS - 1) / ER_ROWS, S), ER_THREADS, 0, st>>>(
+    evict_rows_kernel<<<dim3(max_keep / ER_ROWS + (max_keep % ER_ROWS != 0), S), ER_THREADS, 0, st>>>(
         out, cu_src, cu_dst, kept, kept_len, max_keep, status);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -45,6 +45,20 @@ __device__ __forceinline__ int find_seq_warp(const int32_t *cu_q, int S, int row
   return lo + n;
 }
 
+// The region of the keys of a query row, for a warp: no tokens for a row outside every
+// sequence (behind the last one of a padded batch), so that it adds nothing to one.
+struct Region {
+  int base, tokens;
+};
+__device__ __forceinline__ Region region_of(const int32_t *cu_q, const int32_t *cu_k, int S,
+                                            int row, int lane) {
+  const int rows = __ldg(cu_q + S);  // beside the search, not after it
+  const int s = find_seq_warp(cu_q, S, row, lane);
+  // the end's address is chosen, not the count (8192 rows of 2048 tokens: 551 us against 561)
+  const int base = __ldg(cu_k + s), end = __ldg(cu_k + s + (row < rows));
+  return {base, end - base};
+}
+
 __device__ __forceinline__ __half2 as_half2(uint32_t w) {
   return *reinterpret_cast<const __half2 *>(&w);
 }

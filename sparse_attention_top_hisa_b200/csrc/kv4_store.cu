@@ -7,7 +7,7 @@
 // lies at 7 * (a 5-bit number) and one of x / s at s * (a 4-bit number): both are 8-bit
 // numbers, so a quotient that is not a tie is at least 2^-8 (relative) from one.  The
 // products with the rounded reciprocals of 7 and s are off by a few 2^-23; rounding them
-// to 12 bits (a / 7) and to a multiple of 2^-12 (x / s, in the FMA that adds 3072) puts
+// to 12 bits (a / 7) and to a multiple of 2^-12 (x / s, in the FMA that adds 1.5 * 2^11) puts
 // ties back where they belong and moves nothing else across one, and a second rounding
 // decides.
 //
@@ -50,10 +50,10 @@ __device__ __forceinline__ uint32_t nibbles(const uint32_t *w, float r) {
   uint32_t sum = 0;
 #pragma unroll
   for (int j = 7; j >= 0; j--) {
-    float t = fmaf((j & 1) ? bf_hi(w[j >> 1]) : bf_lo(w[j >> 1]), r, 3072.f);
-    if (CLAMP) t = fminf(fmaxf(t, 3065.f), 3079.f);
+    float t = fmaf((j & 1) ? bf_hi(w[j >> 1]) : bf_lo(w[j >> 1]), r, 0x1.8p11f);
+    if (CLAMP) t = fminf(fmaxf(t, 0x1.8p11f - 7.f), 0x1.8p11f + 7.f);
     // 1.5 * 2^23 + 8 + q: rounds to a whole number, whose bits are a constant and q + 8
-    t += 12582912.f + 8.f - 3072.f;
+    t += 0x1.8p23f + 8.f - 0x1.8p11f;
     sum = sum * 16u + __float_as_uint(t);
   }
   return sum - 0x11111111u * 0x4B400000u;
@@ -205,7 +205,8 @@ kv4_load_kernel(const uint8_t *__restrict__ kv4, const uint8_t *__restrict__ kv4
 }
 
 // Rows of a warp: 4 once that still leaves two CTAs for every SM (16 rows of a CTA).  Stored
-// and read back, 131072 rows take 42 us with 2, 39 with 4 and 43 with 8.
+// and read back, 131072 rows take 37 us with 2, 34 with 4 and 37 with 8; 16 rows 4.9 with 2,
+// 6.2 with 4 and 8.5 with 8.
 static int rows_per_unit(int total_q, int num_sms) { return total_q >= 32 * num_sms ? 2 : 1; }
 static int store_grid(int total_q, int r) {
   const int per = KVS_WARPS * 2 * r;

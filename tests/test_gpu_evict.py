@@ -387,3 +387,20 @@ def test_select_and_move_in_a_graph():
             want = kv4_ref.evict_select(hw[at:at + hl[s]], int(hl[s]), [500, 700][s], 4, 64)
             assert int(n[s]) == len(want)
             assert np.array_equal(x[at:at + len(want)].cpu().numpy(), hx[at + want])
+
+
+def test_rows_with_the_largest_max_keep():
+    """max_keep only has to be at least every count."""
+    h = H()
+    cu, kept = dev_i32([0, 256]), torch.arange(3, 259, dtype=torch.int32, device="cuda")
+    a = torch.arange(256, dtype=torch.int32, device="cuda")
+    for most in (2 ** 31 - 1, 2 ** 31 - 128):
+        b = torch.zeros_like(a)
+        h.hisa_device_status(clear=True)
+        h.hisa_evict_rows([a], [b], cu, cu, kept, dev_i32([200]), most)
+        assert h.hisa_device_status() == 0
+        assert torch.equal(b[:200], a[3:203]) and not b[200:].any()
+        b = a.clone()
+        h.hisa_evict_rows([b], [b], cu, cu, kept, dev_i32([200]), most)
+        assert h.hisa_device_status() == 0
+        assert torch.equal(b[:200], a[3:203]) and torch.equal(b[200:], a[200:])

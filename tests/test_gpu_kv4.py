@@ -561,3 +561,37 @@ def test_empty_calls():
     with pytest.raises(h.HisaError):  # no entry per row at all
         h.hisa_sparse_attention_kv4(c.q, *dev, dev_i32(np.zeros((2, 0))), dev_i32(c.cu_q), cu_k,
                                     0.1)
+
+
+@pytest.mark.parametrize("heads,topk,news", [(16, 300, [3, 2]), (16, 40, [3000, 2]),
+                                             (20, 300, [3, 2]), (20, 40, [3000, 2])])
+def test_rows_behind_the_last_sequence_add_nothing(heads, topk, news):
+    """A padded batch: rows past cu_seqlens_q[S] have no tokens, whatever their indices say."""
+    h = H()
+    pad = 7
+    c = Case(heads + topk, heads, topk, [4000, 500], news)
+    n = len(c.idx)
+    rng = np.random.Generator(np.random.PCG64(5))
+    k, v = bf16(rng.standard_normal((c.rows, DIM))), bf16(rng.standard_normal((c.rows, DIM)))
+    q = torch.cat([c.q, c.q[:pad - 2], c.q[:2]])
+    dev = [torch.from_numpy(x).cuda() for x in (c.codes, c.scales)]
+    cu_q, cu_k = dev_i32(c.cu_q), dev_i32(c.cu_k)
+    want, _, want_w = c.check()
+    lse_bf = torch.empty(n, heads, device="cuda")
+    h.hisa_sparse_attention(c.q, k, v, dev_i32(c.idx), cu_q, cu_k, c.scale, lse=lse_bf)
+    want_tw = torch.zeros(c.rows, dtype=torch.int64, device="cuda")
+    h.hisa_token_weights(c.q, k, dev_i32(c.idx), lse_bf, cu_q, cu_k, c.scale, want_tw)
+    for fill, status in ((-1, 0), (3, 1 << 1)):
+        idx = dev_i32(np.concatenate([c.idx, np.full((pad, topk), fill, np.int32)]))
+        h.hisa_device_status(clear=True)
+        lse = torch.empty(n + pad, heads, device="cuda")
+        w = torch.zeros(c.rows, dtype=torch.int64, device="cuda")
+        out = h.hisa_sparse_attention_kv4(q, *dev, idx, cu_q, cu_k, c.scale, lse=lse, weights=w)
+        assert h.hisa_device_status(clear=True) == status
+        assert np.array_equal(f64(out[:n]), want) and not out[n:].any()
+        assert np.array_equal(w.cpu().numpy(), want_w) and torch.isneginf(lse[n:]).all()
+        tw = torch.zeros_like(w)
+        lse_pad = torch.cat([lse_bf, torch.ones(pad, heads, device="cuda")])
+        h.hisa_token_weights(q, k, idx, lse_pad, cu_q, cu_k, c.scale, tw)
+        assert h.hisa_device_status(clear=True) == status
+        assert torch.equal(tw, want_tw)

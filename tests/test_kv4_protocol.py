@@ -156,3 +156,9 @@ def test_binding_refuses_host_tensors():
         H.hisa_sparse_attention_kv4(x.view(128, 1, 128), kv, sc, cu.view(1, 2), cu, cu, 1.0)
     with pytest.raises(ValueError, match="CUDA tensor"):
         H.hisa_evict_select(torch.zeros(128, dtype=torch.int64), cu, None, cu[1:], 128, 0, 0)
+
+
+def test_index_rows_past_the_limit_are_refused(lib):
+    big = (1 << 28) + 1
+    assert lib.hisa_sparse_attention_kv4(D, D, D, D, D, D, 1, 4, 8, big, F(0.1), D, D, D, None) == 1
+    assert lib.hisa_token_weights(D, D, D, D, D, D, 1, 4, 8, big, F(0.1), D, None) == 1
