@@ -43,26 +43,43 @@ static_assert(EV_COARSE == 64 && EV_THREADS == 1024, "two coarse bins per warp a
 struct EvictShared {
   int hist[2][EV_BINS];
   int coarse[2][EV_COARSE];
-  unsigned long long red[2][EV_THREADS / 32];
+  uint32_t red[EV_THREADS / 32][2];  // counts of the warps
   int odd;                       // a weight below 0 or of 2^58 and more among this CTA's
   int bin, above, in_bin;        // the bin in which the count passes, the counts above and in it
+  int2 ahead;                    // of those, the counts of the CTAs before this one
   int any_odd;                   // of the cluster
-  int2 counts;                   // middle and fixed tokens above the threshold, ties
 };
+
+// Barrier of the cluster in two halves, for all threads of its CTAs.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
 
 // Warp 0: the bin, from the highest, in which the counts of the cluster's C CTAs pass `left`.
 // Two steps of one remote look each: 64 coarse bins, then the 32 bins of one of them.
-__device__ __forceinline__ void find_bin(cg::cluster_group &cl, EvictShared &sm, int C, int buf,
-                                         int left, int lane) {
-  int hi = 0, lo = 0;  // coarse bins 63 - 2 lane and 62 - 2 lane
+__device__ __forceinline__ void find_bin(cg::cluster_group &cl, EvictShared &sm, int C, int me,
+                                         int buf, int left, int lane) {
+  int hi = 0, lo = 0;    // coarse bins 63 - 2 lane and 62 - 2 lane
+  int phi = 0, plo = 0;  // the same of the CTAs before this one
+  int2 h2[EV_MAX_CLUSTER] = {};  // all in flight before one is used
+  if (C == 1)
+    h2[0] = *reinterpret_cast<const int2 *>(sm.coarse[buf] + 62 - 2 * lane);
+  else
 #pragma unroll
-  for (int r = 0; r < EV_MAX_CLUSTER; r++)
-    if (r < C) {
-      const int2 h =
-          *reinterpret_cast<const int2 *>(cl.map_shared_rank(sm.coarse[buf], r) + 62 - 2 * lane);
-      lo += h.x;
-      hi += h.y;
-    }
+    for (int r = 0; r < EV_MAX_CLUSTER; r++)
+      if (r < C)
+        h2[r] = *reinterpret_cast<const int2 *>(cl.map_shared_rank(sm.coarse[buf], r) + 62 -
+                                                2 * lane);
+#pragma unroll
+  for (int r = 0; r < EV_MAX_CLUSTER; r++) {
+    lo += h2[r].x;
+    hi += h2[r].y;
+    plo += r < me ? h2[r].x : 0;
+    phi += r < me ? h2[r].y : 0;
+  }
   int x = hi + lo;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -75,63 +92,113 @@ __device__ __forceinline__ void find_bin(cg::cluster_group &cl, EvictShared &sm,
   const bool upper = before + hi >= left;
   const int cb = __shfl_sync(0xffffffffu, upper ? 63 - 2 * lane : 62 - 2 * lane, src);
   const int above = __shfl_sync(0xffffffffu, upper ? before : before + hi, src);
-  int n = 0;  // bin 31 - lane of the coarse bin
+  int n = 0, pn = 0;  // bin 31 - lane of the coarse bin
+  int h1[EV_MAX_CLUSTER] = {};
+  if (C == 1)
+    h1[0] = sm.hist[buf][cb * EV_FINE + 31 - lane];
+  else
 #pragma unroll
-  for (int r = 0; r < EV_MAX_CLUSTER; r++)
-    if (r < C) n += cl.map_shared_rank(sm.hist[buf], r)[cb * EV_FINE + 31 - lane];
+    for (int r = 0; r < EV_MAX_CLUSTER; r++)
+      if (r < C) h1[r] = cl.map_shared_rank(sm.hist[buf], r)[cb * EV_FINE + 31 - lane];
+#pragma unroll
+  for (int r = 0; r < EV_MAX_CLUSTER; r++) {
+    n += h1[r];
+    pn += r < me ? h1[r] : 0;
+  }
+  int p = lane < src ? phi + plo : lane == src && !upper ? phi : 0;
   x = n;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, x, d);
     if (lane >= d) x += y;
   }
-  if (above + x - n < left && above + x >= left) {
+  const bool here = above + x - n < left && above + x >= left;
+  const int w = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  p = __reduce_add_sync(0xffffffffu, p + (lane < w ? pn : 0));
+  if (here) {
     sm.bin = cb * EV_FINE + 31 - lane;
     sm.above = above + x - n;
     sm.in_bin = n;
+    sm.ahead = make_int2(p, pn);
   }
 }
 
-// Exclusive sums over the block's threads of four 16-bit fields each; *sa, *sb the totals.
-__device__ __forceinline__ void scan_fields(unsigned long long &a, unsigned long long &b,
-                                            unsigned long long (*red)[EV_THREADS / 32],
-                                            unsigned long long *sa, unsigned long long *sb) {
+// Exclusive sums over the block's threads of a thread's counts a and e (at most EV_PER each) of
+// NG groups, packed in bytes: at most 128 in a warp.  Of the whole block two 16-bit fields share
+// a word.  pa, pe: the sums; sa, se: the totals.
+template <int NG>
+__device__ __forceinline__ void scan_counts(uint32_t a, uint32_t e, uint32_t (*red)[2],
+                                            int (&pa)[NG], int (&pe)[NG], int (&sa)[NG],
+                                            int (&se)[NG]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long x = a, y = b;
+  uint32_t x = a, y = e;
+  if (NG <= 2) x |= e << 16;  // one word has room for both
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const unsigned long long u = __shfl_up_sync(0xffffffffu, x, d);
-    const unsigned long long v = __shfl_up_sync(0xffffffffu, y, d);
-    if (lane >= d) {
-      x += u;
-      y += v;
+    const uint32_t u = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += u;
+    if (NG > 2) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, y, d);
+      if (lane >= d) y += v;
     }
   }
   if (lane == 31) {
-    red[0][warp] = x;
-    red[1][warp] = y;
+    red[warp][0] = x;
+    red[warp][1] = NG <= 2 ? x >> 16 : y;
   }
   __syncthreads();
+  if (NG <= 2) y = x >> 16;
   // every warp sums the warps before it: lane w looks at warp w
-  unsigned long long p = red[0][lane], q = red[1][lane];
-  unsigned long long pa = lane < warp ? p : 0ull, qa = lane < warp ? q : 0ull;
+  const uint2 r = *reinterpret_cast<const uint2 *>(red[lane]);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    p += __shfl_xor_sync(0xffffffffu, p, d);
-    q += __shfl_xor_sync(0xffffffffu, q, d);
-    pa += __shfl_xor_sync(0xffffffffu, pa, d);
-    qa += __shfl_xor_sync(0xffffffffu, qa, d);
+  for (int i = 0; i < NG; i += 2) {  // groups i and i + 1
+    const uint32_t ra = __byte_perm(r.x, 0u, i ? 0x4342 : 0x4140);
+    const uint32_t re = __byte_perm(r.y, 0u, i ? 0x4342 : 0x4140);
+    const uint32_t ta = __reduce_add_sync(0xffffffffu, ra);
+    const uint32_t te = __reduce_add_sync(0xffffffffu, re);
+    const uint32_t ba = __reduce_add_sync(0xffffffffu, lane < warp ? ra : 0u);
+    const uint32_t be = __reduce_add_sync(0xffffffffu, lane < warp ? re : 0u);
+#pragma unroll
+    for (int j = i; j < NG && j < i + 2; j++) {
+      const int h = 16 * (j - i), f = 8 * j;
+      sa[j] = (ta >> h) & 0xFFFF;
+      se[j] = (te >> h) & 0xFFFF;
+      pa[j] = ((ba >> h) & 0xFFFF) + ((x >> f) & 0xFF) - ((a >> f) & 0xFF);
+      pe[j] = ((be >> h) & 0xFFFF) + ((y >> f) & 0xFF) - ((e >> f) & 0xFF);
+    }
   }
-  a = pa + x - a;
-  b = qa + y - b;
-  *sa = p;
-  *sb = q;
   __syncthreads();
+}
+
+template <int N>
+struct Const {
+  static constexpr int v = N;
+};
+
+__device__ __forceinline__ void load_four(const long long *p, unsigned long long (&w)[EV_PER]) {
+  asm("ld.global.nc.v4.b64 {%0, %1, %2, %3}, [%4];"
+      : "=l"(w[0]), "=l"(w[1]), "=l"(w[2]), "=l"(w[3])
+      : "l"(p));
+}
+
+// Bits n0 .. n1 - 1 of a group's four, of tokens i .. i + 3: those in [from, to)
+__device__ __forceinline__ uint32_t group_bits(int i, int from, int to) {
+  const int n0 = min(max(from - i, 0), EV_PER), n1 = min(max(to - i, 0), EV_PER);
+  return ((1u << n1) - 1u) & ~((1u << n0) - 1u);
 }
 
 // A sequence belongs to a cluster, its tokens in order to the cluster's CTAs; of a CTA's, a
 // thread has EV_PER consecutive ones of every group of EV_STRIDE.  G groups: their keys
-// stay in registers; G = 0: any number of groups, every pass reads the weights again.
+// stay in registers, 0 for tokens that are not in question; G = 0: any number of groups,
+// every pass reads the weights again.
+//
+// What bounds it: latency, and with several groups the instructions of a token.  Of 31000
+// cycles for one sequence of 131072 tokens (eight CTAs, four groups) the loads and the keys
+// take 6400, the counts of its two passes 2700 and 1900, each look for the bin 3100, each
+// cluster barrier 1000 to 1500, the positions 8000; 1100 tokens of one CTA take 12000 in all.
+// So every pass has code of its own, in which the shifts of the 64-bit keys are constants, and
+// the counts of the CTAs before this one come with the look for the bin instead of an exchange
+// at the end (32.1 us before these two, 24.8 with them, the rows' 6 us among them).
 template <int G>
 __global__ void __launch_bounds__(EV_THREADS)
 evict_select_kernel(const long long *__restrict__ weights, const int32_t *__restrict__ cu_k,
@@ -165,69 +232,119 @@ evict_select_kernel(const long long *__restrict__ weights, const int32_t *__rest
   // this CTA's tokens: [c0, c1), a whole number of EV_PER but for the last
   const int chunk = ((len + C - 1) / C + EV_PER - 1) / EV_PER * EV_PER;
   const int c0 = min(len, me * chunk), c1 = min(len, c0 + chunk);
-  const int m0 = max(c0, lo), m1 = min(c1, hi);  // its middle tokens
-  const int first = c0 + tid * EV_PER;           // this thread's first of group 0
+  const int m0 = max(c0, lo), m1 = max(m0, min(c1, hi));  // its middle tokens
+  const int first = c0 + tid * EV_PER;                    // this thread's first of group 0
   const int groups = G > 0 ? G : (c1 - c0 + EV_STRIDE - 1) / EV_STRIDE;
+  auto middle = [&](int i) { return (uint32_t)(i - m0) < (uint32_t)(m1 - m0); };
 
-  unsigned long long kx[G > 0 ? G : 1][EV_PER];
+  constexpr int KG = G > 0 ? G : 1;
+  unsigned long long kx[KG][EV_PER];
   bool plain = false;
-  // fn(key) for every middle token of this thread
-  auto each = [&](auto fn) {
+  // a thread's four weights of a group are one load where they are all its CTA's and
+  // aligned (four groups: 4400 cycles; 6800 by single ones, 32 bytes apart in a warp)
+  const bool wide = reinterpret_cast<uintptr_t>(ws) % (EV_PER * sizeof(*ws)) == 0;
+  auto read = [&](int i, unsigned long long (&w)[EV_PER]) {
+    if (wide && i + EV_PER <= c1) {
+      load_four(ws + i, w);
 #pragma unroll
-    for (int gr = 0; gr < groups; gr++)
+      for (int u = 0; u < EV_PER; u++) w[u] = middle(i + u) ? w[u] : 0ull;
+    } else {
+#pragma unroll
+      for (int u = 0; u < EV_PER; u++)
+        w[u] = middle(i + u) ? (unsigned long long)__ldg(ws + i + u) : 0ull;
+    }
+  };
+  // the weights, as they are, of this thread's tokens; the bits of all of them
+  auto load = [&] {
+    unsigned long long o = 0ull;
+#pragma unroll
+    for (int gr = 0; gr < groups; gr++) {
+      unsigned long long w[EV_PER];
+      read(first + gr * EV_STRIDE, w);
 #pragma unroll
       for (int u = 0; u < EV_PER; u++) {
-        const int i = first + gr * EV_STRIDE + u;
-        if (i >= m0 && i < m1) fn(G > 0 ? kx[G > 0 ? gr : 0][u] : weight_key(__ldg(ws + i), plain));
+        if (G > 0) kx[G > 0 ? gr : 0][u] = w[u];
+        o |= w[u];
       }
+    }
+    return o;
+  };
+  int outside = 0;  // tokens of this thread with a key of 0 that are not in question
+  auto to_keys = [&] {
+    if (G == 0) return;
+    outside = KG * EV_PER;
+#pragma unroll
+    for (int gr = 0; gr < KG; gr++) {
+      const int i = first + gr * EV_STRIDE;
+      outside -= __popc(group_bits(i, m0, m1));
+#pragma unroll
+      for (int u = 0; u < EV_PER; u++)
+        kx[gr][u] = plain && !middle(i + u) ? 0ull : weight_key((long long)kx[gr][u], plain);
+    }
+  };
+  // fn(key) for every middle token of this thread (G > 0: for every other one fn(0))
+  auto each = [&](auto fn) {
+#pragma unroll
+    for (int gr = 0; gr < groups; gr++) {
+      const int i = first + gr * EV_STRIDE;
+      unsigned long long w[EV_PER];
+      if (G == 0) read(i, w);
+#pragma unroll
+      for (int u = 0; u < EV_PER; u++) {
+        if (G > 0)
+          fn(kx[G > 0 ? gr : 0][u]);
+        else if (middle(i + u))
+          fn(weight_key((long long)w[u], plain));
+      }
+    }
   };
 
   // keys above `thr` stay, of those equal to it the first `ties`
-  unsigned long long thr = ~0ull;
-  int ties = 0;
-  if (quota > 0) {
-    unsigned long long o = 0ull;
-#pragma unroll
-    for (int gr = 0; gr < groups; gr++)
-#pragma unroll
-      for (int u = 0; u < EV_PER; u++) {
-        const int i = first + gr * EV_STRIDE + u;
-        const unsigned long long w =
-            i >= m0 && i < m1 ? (unsigned long long)__ldg(ws + i) : 0ull;
-        if (G > 0) kx[G > 0 ? gr : 0][u] = w;
-        o |= w;
+  unsigned long long thr = ~0ull, prefix = 0ull;
+  int ties = 0, left = quota, buf = 0;
+  // tokens before this CTA's that stay whatever the ties (the fixed ones to begin with), and
+  // ties
+  int above = min(c0, lo) + max(0, c0 - hi), equal = 0;
+  // counts the bits SHIFT .. TOP - 1 of the keys that are `prefix` above them
+  auto count = [&](auto top_bit) {
+    constexpr int TOP = decltype(top_bit)::v, SHIFT = TOP > EV_BITS ? TOP - EV_BITS : 0;
+    int *hist = sm.hist[buf];
+    int zero = 0;  // tokens that nothing attended to: often many, and all in one bin
+    each([&](unsigned long long k) {
+      if (TOP == 64) {
+        if (k == 0ull)
+          zero++;
+        else
+          atomicAdd(&hist[(int)(k >> SHIFT)], 1);
+      } else {
+        const unsigned long long d = k ^ prefix;
+        if ((d >> (TOP % 64)) == 0) atomicAdd(&hist[(int)(d >> SHIFT)], 1);
       }
+    });
+    if (prefix == 0ull) {  // else no key of this pass is 0
+      zero = __reduce_add_sync(0xffffffffu, zero - outside);
+      if (lane == 0 && zero) atomicAdd(&hist[0], zero);
+    }
+  };
+  if (quota > 0) {
+    const unsigned long long o = load();
     if (tid == 0) sm.odd = 0;
     for (int i = tid; i < EV_BINS; i += EV_THREADS) sm.hist[0][i] = 0;
     __syncthreads();
     if (o >> 58) sm.odd = 1;
-    auto to_keys = [&] {
-      if (G > 0) {
-#pragma unroll
-        for (int gr = 0; gr < (G > 0 ? G : 1); gr++)
-#pragma unroll
-          for (int u = 0; u < EV_PER; u++) kx[gr][u] = weight_key((long long)kx[gr][u], plain);
-      }
-    };
     to_keys();
-    unsigned long long prefix = 0ull;
-    int left = quota, top = 64;  // bits of the keys that are not known yet
-    for (int pass = 0; top > 0; pass++) {
-      const int shift = max(0, top - EV_BITS), nb = top - shift, buf = pass & 1;
-      int *hist = sm.hist[buf];
-      int zero = 0;  // tokens that nothing attended to: often many, and all in one bin
-      each([&](unsigned long long k) {
-        const unsigned long long d = k ^ prefix;
-        if (k == 0ull)
-          zero++;
-        else if (top == 64 || (d >> top) == 0)
-          atomicAdd(&hist[(int)((d >> shift) & ((1u << nb) - 1))], 1);
-      });
-      if (prefix == 0ull) {  // else no bucket of this pass holds the key 0
-        zero = __reduce_add_sync(0xffffffffu, zero);
-        if (lane == 0 && zero) atomicAdd(&hist[0], zero);
+    for (int top = 64;;) {  // bits of the keys that are not known yet
+      switch (top) {
+        case 64: count(Const<64>()); break;
+        case 53: count(Const<53>()); break;
+        case 42: count(Const<42>()); break;
+        case 31: count(Const<31>()); break;
+        case 20: count(Const<20>()); break;
+        default: count(Const<9>());
       }
+      const int shift = max(0, top - EV_BITS);
       __syncthreads();
+      const int *hist = sm.hist[buf];
       const int n0 = __reduce_add_sync(0xffffffffu, hist[2 * warp * EV_FINE + lane]);
       const int n1 = __reduce_add_sync(0xffffffffu, hist[(2 * warp + 1) * EV_FINE + lane]);
       if (lane < 2) sm.coarse[buf][2 * warp + lane] = lane ? n1 : n0;
@@ -237,28 +354,21 @@ evict_select_kernel(const long long *__restrict__ weights, const int32_t *__rest
       else
         __syncthreads();
       if (warp == 0) {
-        if (pass == 0) {
+        if (top == 64) {
           const int odd = lane < C ? *cl.map_shared_rank(&sm.odd, lane) : 0;
           const bool any = __any_sync(0xffffffffu, odd != 0);
           if (lane == 0) sm.any_odd = any;
         }
-        find_bin(cl, sm, C, buf, left, lane);
+        find_bin(cl, sm, C, me, buf, left, lane);
       }
-      int *next = sm.hist[buf ^ 1];
+      buf ^= 1;
+      int *next = sm.hist[buf];
       next[tid] = next[tid + EV_THREADS] = 0;
       __syncthreads();
-      if (pass == 0 && sm.any_odd && !plain) {  // once more, on the weights as they are
+      if (top == 64 && sm.any_odd && !plain) {  // again, on the weights as they are
         plain = true;
-        if (G > 0) {
-#pragma unroll
-          for (int gr = 0; gr < (G > 0 ? G : 1); gr++)
-#pragma unroll
-            for (int u = 0; u < EV_PER; u++) {
-              const int i = first + gr * EV_STRIDE + u;
-              kx[gr][u] = i >= m0 && i < m1 ? (unsigned long long)__ldg(ws + i) : 0ull;
-            }
-          to_keys();
-        }
+        load();
+        to_keys();
         continue;
       }
       left -= sm.above;
@@ -266,88 +376,77 @@ evict_select_kernel(const long long *__restrict__ weights, const int32_t *__rest
       top = shift;
       // the bin stays whole, or (exponent 0) holds zeros only
       const bool whole = sm.in_bin == left, zeros = !plain && (prefix >> 58) == 0;
+      const int2 ahead = sm.ahead;
+      above += ahead.x;
       __syncthreads();
-      if (whole) break;
-      if (zeros) top = 0;
+      if (whole) {
+        thr = prefix - 1;  // prefix > 0: more tokens than the quota, so a lower key exists
+        above += ahead.y;
+        break;
+      }
+      if (zeros || top == 0) {
+        thr = prefix;
+        ties = left;
+        equal = ahead.y;
+        break;
+      }
     }
-    if (top > 0) {  // the whole bucket stays
-      thr = prefix - 1;  // prefix > 0: more tokens than the quota, so a lower key exists
-    } else {
-      thr = prefix;
-      ties = left;
-    }
+    if (C > 1) cluster_arrive();  // this CTA reads the others' counts no more
   }
-  // Counts of this CTA's tokens above the threshold (the fixed ones among them) and equal
-  // to it, for the CTAs behind it; then the positions.
-  int above = 0, equal = 0;
-  if (C > 1) {
-    int gt = 0, eq = 0;
-    if (quota > 0)
-      each([&](unsigned long long k) {
-        gt += k > thr;
-        eq += k == thr;
-      });
-    gt = __reduce_add_sync(0xffffffffu, gt);
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    if (lane == 0) sm.red[0][warp] = ((unsigned long long)(uint32_t)eq << 32) | (uint32_t)gt;
-    __syncthreads();
-    if (warp == 0) {
-      const unsigned long long v = sm.red[0][lane];
-      gt = __reduce_add_sync(0xffffffffu, (int)(uint32_t)v) + (c1 - c0) - max(0, m1 - m0);
-      eq = __reduce_add_sync(0xffffffffu, (int)(v >> 32));
-      if (lane == 0) sm.counts = make_int2(gt, eq);
-    }
-    cl.sync();
-    int2 v = make_int2(0, 0);
-    if (lane < me) v = *cl.map_shared_rank(&sm.counts, lane);
-    above = __reduce_add_sync(0xffffffffu, v.x);
-    equal = __reduce_add_sync(0xffffffffu, v.y);
-  }
-  // EV_MAX_GROUPS groups at a time: four bits of a thread's tokens per group, one scan
-  for (int g0 = 0; g0 < groups; g0 += EV_MAX_GROUPS) {
-    uint32_t fg = 0, fe = 0;
-    unsigned long long a = 0, e = 0, sa, se;
+  // Bits of this thread's tokens of NG groups from g0 on, four of a group: those above the
+  // threshold, the fixed ones among them, and those equal to it.
+  constexpr int NG = G > 0 ? G : EV_MAX_GROUPS;
+  auto classify = [&](int g0, uint32_t &fg, uint32_t &fe) {
+    fg = fe = 0;
 #pragma unroll
-    for (int gr = 0; gr < (G > 0 ? G : EV_MAX_GROUPS); gr++) {
+    for (int gr = 0; gr < NG; gr++) {
+      const int i = first + (g0 + gr) * EV_STRIDE;
+      const uint32_t mid = group_bits(i, m0, m1) << (4 * gr);
+      uint32_t above = 0, equal = 0;
+      if (quota > 0) {
+        unsigned long long w[EV_PER];
+        if (G == 0) read(i, w);
 #pragma unroll
-      for (int u = 0; u < EV_PER; u++) {
-        const int i = first + (g0 + gr) * EV_STRIDE + u;
-        bool isg = false, ise = false;
-        if (i < c1) {
-          if (i < lo || i >= hi) {
-            isg = true;
-          } else if (quota > 0) {
-            const unsigned long long k =
-                G > 0 ? kx[G > 0 ? gr : 0][u] : weight_key(__ldg(ws + i), plain);
-            isg = k > thr;
-            ise = k == thr;
-          }
+        for (int u = 0; u < EV_PER; u++) {
+          const unsigned long long k =
+              G > 0 ? kx[G > 0 ? gr : 0][u] : weight_key((long long)w[u], plain);
+          if (k > thr) above |= 1u << (4 * gr + u);
+          if (ties > 0 && k == thr) equal |= 1u << (4 * gr + u);
         }
-        fg |= (uint32_t)isg << (4 * gr + u);
-        fe |= (uint32_t)ise << (4 * gr + u);
       }
-      a |= (unsigned long long)__popc((fg >> (4 * gr)) & 15u) << (16 * gr);
-      e |= (unsigned long long)__popc((fe >> (4 * gr)) & 15u) << (16 * gr);
+      fg |= (above & mid) | ((group_bits(i, c0, c1) << (4 * gr)) & ~mid);
+      fe |= equal & mid;
     }
-    scan_fields(a, e, sm.red, &sa, &se);
+  };
+  uint32_t fg = 0, fe = 0;
+  if (G > 0) classify(0, fg, fe);
+  // the positions: NG groups at a time, one scan of their counts
+  for (int g0 = 0; g0 < groups; g0 += NG) {
+    if (G == 0) classify(g0, fg, fe);
+    uint32_t a = 0, e = 0;
 #pragma unroll
-    for (int gr = 0; gr < (G > 0 ? G : EV_MAX_GROUPS); gr++) {
-      int at = above + (int)((a >> (16 * gr)) & 0xFFFF);
-      int et = equal + (int)((e >> (16 * gr)) & 0xFFFF);
+    for (int gr = 0; gr < NG; gr++) {
+      a |= __popc((fg >> (4 * gr)) & 15u) << (8 * gr);
+      e |= __popc((fe >> (4 * gr)) & 15u) << (8 * gr);
+    }
+    int pa[NG], pe[NG], sa[NG], se[NG];
+    scan_counts<NG>(a, e, sm.red, pa, pe, sa, se);
+#pragma unroll
+    for (int gr = 0; gr < NG; gr++) {
+      int et = equal + pe[gr], at = above + pa[gr] + min(et, ties);
 #pragma unroll
       for (int u = 0; u < EV_PER; u++) {
-        const bool isg = (fg >> (4 * gr + u)) & 1u, ise = (fe >> (4 * gr + u)) & 1u;
-        if (isg || (ise && et < ties))
-          ks[at + min(et, ties)] = first + (g0 + gr) * EV_STRIDE + u;
-        at += isg;
-        et += ise;
+        const bool tie = (fe >> (4 * gr + u)) & 1u;
+        if (((fg >> (4 * gr + u)) & 1u) || (tie && et < ties))
+          ks[at++] = first + (g0 + gr) * EV_STRIDE + u;
+        et += tie;
       }
-      above += (int)((sa >> (16 * gr)) & 0xFFFF);
-      equal += (int)((se >> (16 * gr)) & 0xFFFF);
+      above += sa[gr];
+      equal += se[gr];
     }
   }
   if (tid == 0 && me == 0) kept_len[s] = budget;
-  if (C > 1) cl.sync();  // no CTA leaves while another reads its counts
+  if (quota > 0 && C > 1) cluster_wait();  // no CTA leaves while another reads its counts
 }
 
 cudaError_t launch_evict_select(const int64_t *weights, const int32_t *cu_k,
