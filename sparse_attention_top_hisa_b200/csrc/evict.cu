@@ -175,10 +175,13 @@ struct Const {
   static constexpr int v = N;
 };
 
+// 32 bytes from an address that is a multiple of 32
 __device__ __forceinline__ void load_four(const long long *p, unsigned long long (&w)[EV_PER]) {
-  asm("ld.global.nc.v4.b64 {%0, %1, %2, %3}, [%4];"
-      : "=l"(w[0]), "=l"(w[1]), "=l"(w[2]), "=l"(w[3])
-      : "l"(p));
+  // volatile: a statement without it may be moved before the check of the alignment
+  asm volatile("ld.global.nc.v4.b64 {%0, %1, %2, %3}, [%4];"
+               : "=l"(w[0]), "=l"(w[1]), "=l"(w[2]), "=l"(w[3])
+               : "l"(p)
+               : "memory");
 }
 
 // Bits n0 .. n1 - 1 of a group's four, of tokens i .. i + 3: those in [from, to)

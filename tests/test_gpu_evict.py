@@ -404,3 +404,23 @@ def test_rows_with_the_largest_max_keep():
         h.hisa_evict_rows([b], [b], cu, cu, kept, dev_i32([200]), most)
         assert h.hisa_device_status() == 0
         assert torch.equal(b[:200], a[3:203]) and torch.equal(b[200:], a[200:])
+
+
+@pytest.mark.parametrize("shift", [1, 2, 3])
+@pytest.mark.parametrize("lens,keep", [([1500, 4097], [700, 4096]), ([70001], [30000]),
+                                       ([150003], [50001])])
+def test_select_weights_at_any_address(lens, keep, shift):
+    """Regions that start at any row, weights aligned to 8 bytes only."""
+    h = H()
+    rng = np.random.Generator(np.random.PCG64(shift + len(lens)))
+    cu = (np.cumsum([0] + [n + 5 for n in lens]) + shift).astype(np.int32)
+    for kind in ("real", "ties", "wide"):
+        w = weights_of(kind, int(cu[-1]), rng)
+        dev = torch.from_numpy(np.concatenate([[0], w]).astype(np.int64)).cuda()[1:]
+        kept, n = h.hisa_evict_select(dev, dev_i32(cu), dev_i32(lens), dev_i32(keep), max(lens), 3,
+                                      50)
+        assert n.tolist() == keep
+        for s, length in enumerate(lens):
+            got = kept[cu[s]:cu[s] + keep[s]].cpu().numpy()
+            want = kv4_ref.evict_select(w[cu[s]:cu[s] + length], length, keep[s], 3, 50)
+            assert np.array_equal(got, want), (kind, s)
