@@ -460,7 +460,9 @@ hisa_status hisa_evict_select(const int64_t *weights, const int32_t *cu_seqlens_
  *   kept, kept_len as hisa_evict_select wrote them (kept strictly ascending per sequence);
  *                  neither may be among the arrays.
  *   max_keep       >= every kept_len (host copy, sizes the grid); 0 launches nothing.
- * Rows past kept_len[s] of a destination region are left as they were.  Afterwards
+ * Rows past kept_len[s] of a destination region are left as they were: accumulated weights
+ * moved in place keep their old numbers there, which new tokens would inherit (clear them, or
+ * move the weights to a cleared array).  Afterwards
  * kept_len is the new seqlens_k (with cu_dst as cu_seqlens_k), and hisa_pool_blocks renews
  * the representatives.  Reported in the device status word: a kept_len that is negative,
  * above max_keep or above its source region, a position outside the region (or, in place,
