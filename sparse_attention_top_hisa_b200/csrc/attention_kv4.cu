@@ -119,28 +119,41 @@ __device__ __forceinline__ void q_shift(uint32_t max_bits, float &up, float &dow
 // and 1 (half 0) or 2 and 3; heads >= H are zeros.  In registers (32 for 16 heads) they
 // left the compiler too few to overlap its work: 663 us instead of 637 for 8192 queries of
 // 16 heads on 2048 tokens each.
-// Each of the W warps that share a query looks at all of it, since it needs the heads' powers
-// of two (f: what takes its raw scores, of heads g and g + 8, to exponents of two), and
-// converts its part; the caller synchronises them.
+// Each of the W warps that share a query looks at all of it (QueryRaw), since it needs the
+// heads' powers of two (f: what takes its raw scores, of heads g and g + 8, to exponents of
+// two), and converts its part; the caller synchronises them.
+template <int MT>
+struct QueryRaw {
+  uint4 w[MT][2][4];  // dimensions 32c .. 32c + 31 of heads g and g + 8
+  __device__ __forceinline__ void load(const uint16_t *__restrict__ q, size_t row, int H,
+                                       int lane) {
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+      for (int r = 0; r < 2; r++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int h = 16 * mt + g + 8 * r;
+          w[mt][r][i] = make_uint4(0u, 0u, 0u, 0u);
+          if (h < H)
+            w[mt][r][i] =
+                __ldg(reinterpret_cast<const uint4 *>(q + (row * H + h) * KV4_DIM + 32 * c) + i);
+        }
+  }
+};
 template <int MT, int W>
-__device__ __forceinline__ void load_query(const uint16_t *__restrict__ q, size_t row, int H,
-                                           float scale, uint4 *qs, int lane, int warp,
-                                           float (&f)[MT][2]) {
-  const int g = lane >> 2, c = lane & 3;
+__device__ __forceinline__ void convert_query(const QueryRaw<MT> &raw, float scale, uint4 *qs,
+                                              int lane, int warp, float (&f)[MT][2]) {
 #pragma unroll
   for (int mt = 0; mt < MT; mt++) {
-    uint4 w[2][4];
+    const auto &w = raw.w[mt];
     float up[2];
 #pragma unroll
     for (int r = 0; r < 2; r++) {
-      const int h = 16 * mt + g + 8 * r;
       uint32_t mx = 0;
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        w[r][i] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < H)
-          w[r][i] =
-              __ldg(reinterpret_cast<const uint4 *>(q + (row * H + h) * KV4_DIM + 32 * c) + i);
         const uint4 v = w[r][i];
         mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
                                    __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
@@ -283,19 +296,27 @@ struct Ring {
   __device__ __forceinline__ void init(const int32_t *row, int e0, int end, int first, int step,
                                        int kbase, int cap, const uint8_t *kv4,
                                        const uint8_t *kv4_scale, uint8_t *mem, int lane) {
+    entries(row, e0, end, first, step, lane);
+    region(kbase, cap, kv4, kv4_scale, mem, lane);
+  }
+  __device__ __forceinline__ void entries(const int32_t *row, int e0, int end, int first, int step,
+                                          int lane) {
     irow = row;
     e1 = end;
     const int steps = end > e0 ? (end - e0 + A4_STEP - 1) / A4_STEP : 0;
     nsteps = steps > first ? (steps - first + step - 1) / step : 0;
     first_e = next_e = e0 + first * A4_STEP + lane;
     stride = step * A4_STEP;
+    bad = false;
+    read();
+  }
+  __device__ __forceinline__ void region(int kbase, int cap, const uint8_t *kv4,
+                                         const uint8_t *kv4_scale, uint8_t *mem, int lane) {
     kcap = cap;
     codes = kv4 + (size_t)kbase * KV4_ROW + (lane & 3) * 16;
     scales = kv4_scale + (size_t)kbase * KV4_NS;
     ring = smem_u32(mem);
     slot = fill = 0;
-    bad = false;
-    read();
   }
   __device__ __forceinline__ void read() {
     next_tok = next_e < e1 ? __ldg(irow + next_e) : -1;
@@ -687,7 +708,9 @@ attn_kv4_rows_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict__
   ring.init(irow, 0, topk, 0, 1, kbase, kcap, kv4, kv4_scale, mem, lane);
   ring.start(lp, lane);
   float f[MT][2];
-  load_query<MT, 1>(q, (size_t)row, H, scale, qs, lane, 0, f);
+  QueryRaw<MT> raw;
+  raw.load(q, (size_t)row, H, lane);
+  convert_query<MT, 1>(raw, scale, qs, lane, 0, f);
   __syncwarp();
   const uint32_t qf = smem_u32(qs + lane);
   Running<MT> st;
@@ -736,11 +759,11 @@ template <int MT>
 struct SplitSmem {
   static constexpr int QBYTES = MT * 4096;
   static constexpr int NH = 16 * MT;
-  // ring of every warp | query fragments | m, l of every warp and head | m, l of the CTA |
-  // merge factors of the cluster
-  static constexpr size_t bytes = (size_t)A4_WARPS * a4_ring(MT) + QBYTES +
-                                  (size_t)A4_WARPS * NH * 8 + (size_t)NH * 8 +
-                                  (size_t)NH * A4_MAX_CLUSTER * 4;
+  // ring of every warp | query fragments | partial outputs from the cluster's CTAs | their m
+  // and l | m, l of every warp and head | m, l of the CTA | merge factors of the cluster
+  static constexpr size_t bytes = (size_t)A4_WARPS * a4_ring(MT) + QBYTES + NH * KV4_DIM * 4 +
+                                  A4_MAX_CLUSTER * NH * 8 + (size_t)A4_WARPS * NH * 8 +
+                                  (size_t)NH * 8 + (size_t)NH * A4_MAX_CLUSTER * 4;
 };
 
 template <int MT, bool WT>
@@ -755,26 +778,34 @@ attn_kv4_split_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict_
   constexpr int NST = a4_stages(MT), RING = a4_ring(MT), NH = 16 * MT;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), me = (int)cl.block_rank();
-  const int row = blockIdx.x / C;
+  const int row = blockIdx.x >> (31 - __clz(C));  // C is a power of two
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2;
   const float NEG = -__int_as_float(0x7f800000);
   uint8_t *qs = a4_smem + A4_WARPS * RING;
-  float *wm = reinterpret_cast<float *>(qs + SplitSmem<MT>::QBYTES);  // [warps][NH]
+  float *recv = reinterpret_cast<float *>(qs + SplitSmem<MT>::QBYTES);  // [C][heads][128]
+  float2 *recv_ml = reinterpret_cast<float2 *>(recv + NH * KV4_DIM);    // [C][NH]
+  float *wm = reinterpret_cast<float *>(recv_ml + A4_MAX_CLUSTER * NH);  // [warps][NH]
   float *wl = wm + A4_WARPS * NH;                                     // [warps][NH]
   float *cm = wl + A4_WARPS * NH, *cs = cm + NH;  // the CTA's maximum and sum per head
   float *xm = cs + NH;                            // factors of the cluster's CTAs [NH][C]
-  const Region rg = region_of(cu_q, cu_k, S, row, lane);
-  const int kbase = rg.base, kcap = rg.tokens;
+  if (C > 1) cluster_arrive();  // this CTA runs: the others may write to it
   const LanePlaces lp(lane);
   const int e0 = me * per_cta, e1 = min(topk, e0 + per_cta);
   const int32_t *irow = idx + (size_t)row * topk;
   uint8_t *mem = a4_smem + warp * RING;
+  // the row's first tokens and the query arrive while the sequence is looked up (14400 cycles
+  // of a CTA against 15100)
   Ring<NST, NST - 1, true> ring;
-  ring.init(irow, e0, e1, warp, A4_WARPS, kbase, kcap, kv4, kv4_scale, mem, lane);
+  ring.entries(irow, e0, e1, warp, A4_WARPS, lane);
+  QueryRaw<MT> raw;
+  raw.load(q, (size_t)row, H, lane);
+  const Region rg = region_of(cu_q, cu_k, S, row, lane);
+  const int kbase = rg.base, kcap = rg.tokens;
+  ring.region(kbase, kcap, kv4, kv4_scale, mem, lane);
   ring.start(lp, lane);
   float f[MT][2];
-  load_query<MT, A4_WARPS>(q, (size_t)row, H, scale, reinterpret_cast<uint4 *>(qs), lane, warp, f);
+  convert_query<MT, A4_WARPS>(raw, scale, reinterpret_cast<uint4 *>(qs), lane, warp, f);
   __syncthreads();
   const uint32_t qf = smem_u32(qs + lane * 16);
   Running<MT> st;
@@ -785,23 +816,37 @@ attn_kv4_split_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict_
   __syncthreads();
   if (tid < NH) join_shares<A4_WARPS>(wm, wl, NH, tid, cm[tid], cs[tid]);
   __syncthreads();
-  // With several CTAs every one sums its own warps first (into the first warp's share, each
-  // value by the thread that read it) and learns the others' maxima and sums; CTA me then
-  // finishes the heads me, me + C, ...
-  float *own = reinterpret_cast<float *>(a4_smem);
+  // With several CTAs every one sums its own warps first and sends the heads r, r + C, ... to
+  // CTA r, which finishes them, and its maxima and sums to all.  Sending leaves one exchange
+  // to wait for, where reading the others' shares took three and a last barrier before the
+  // shared memory may go (16 rows of 2048 tokens and 16 heads: 15100 cycles against 16600).
   if (C > 1) {
-    for (int x = tid; x < H * (KV4_DIM / 4); x += A4_THREADS) {
-      const int h = x >> 5, at = h * A4_OSTRIDE + 4 * (x & 31);
-      *reinterpret_cast<float4 *>(own + at) = sum_shares<A4_WARPS>(a4_smem, RING, wm, NH, h, at);
+    const int lc = 31 - __clz(C);
+    const int HL = (H + C - 1) >> lc;  // heads of a CTA; C * HL <= NH
+    cluster_wait();
+    for (int x = tid; x < C * NH; x += A4_THREADS) {
+      const int r = x / NH, h = x % NH;
+      cl.map_shared_rank(recv_ml, r)[me * NH + h] = make_float2(cm[h], cs[h]);
+    }
+#pragma unroll
+    for (int i = 0; i < NH * (KV4_DIM / 4) / A4_THREADS; i++) {
+      const int x = tid + i * A4_THREADS, h = x >> 5, b = (x >> 3) & 3, u = x & 7;
+      if (h < H) {
+        const float4 v = sum_shares<A4_WARPS>(a4_smem, RING, wm, NH, h,
+                                              h * A4_OSTRIDE + 32 * b + 4 * (u ^ (2 * b)));
+        *reinterpret_cast<float4 *>(cl.map_shared_rank(recv, h & (C - 1)) +
+                                    (me * HL + (h >> lc)) * KV4_DIM + 32 * b + 4 * u) = v;
+      }
     }
     cl.sync();
     if (tid < H) {
       float mr[A4_MAX_CLUSTER], lr[A4_MAX_CLUSTER], mx = NEG, sum = 0.f;
 #pragma unroll
       for (int r = 0; r < A4_MAX_CLUSTER; r++) {
-        mr[r] = r < C ? cl.map_shared_rank(cm, r)[tid] : NEG;
-        lr[r] = r < C ? cl.map_shared_rank(cs, r)[tid] : 0.f;
-        mx = fmaxf(mx, mr[r]);
+        const float2 v = r < C ? recv_ml[r * NH + tid] : make_float2(NEG, 0.f);
+        mr[r] = v.x;
+        lr[r] = v.y;
+        mx = fmaxf(mx, v.x);
       }
 #pragma unroll
       for (int r = 0; r < A4_MAX_CLUSTER; r++) {
@@ -812,24 +857,21 @@ attn_kv4_split_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict_
 #pragma unroll
       for (int r = 0; r < A4_MAX_CLUSTER; r++)
         if (r < C) xm[tid * A4_MAX_CLUSTER + r] = mr[r] * inv;
-      if (lse && tid % C == me) lse[(size_t)row * H + tid] = lse_of(mx, sum);
+      if (lse && (tid & (C - 1)) == me) lse[(size_t)row * H + tid] = lse_of(mx, sum);
       wm[tid] = mx;  // the warps' factors are not needed any more
       wl[tid] = inv;
     }
     __syncthreads();
-    const int nloc = me < H ? (H - me + C - 1) / C : 0;
+    const int nloc = me < H ? (H - me + C - 1) >> lc : 0;
     for (int x = tid; x < nloc * (KV4_DIM / 4); x += A4_THREADS) {
-      const int h = me + C * (x >> 5), b = (x >> 3) & 3, u = x & 7;
-      const int at = h * A4_OSTRIDE + 32 * b + 4 * (u ^ (2 * b));
-      float4 part[A4_MAX_CLUSTER];
-#pragma unroll
-      for (int r = 0; r < A4_MAX_CLUSTER; r++)
-        if (r < C) part[r] = *reinterpret_cast<const float4 *>(cl.map_shared_rank(own, r) + at);
+      const int hl = x >> 5, h = me + C * hl, d = 4 * (x & 31);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int r = 0; r < A4_MAX_CLUSTER; r++)
-        if (r < C) add_share(acc, xm[h * A4_MAX_CLUSTER + r], part[r]);
-      store_out(out + ((size_t)row * H + h) * KV4_DIM + 32 * b + 4 * u, acc, 1.f);
+        if (r < C)
+          add_share(acc, xm[h * A4_MAX_CLUSTER + r],
+                    *reinterpret_cast<const float4 *>(recv + (r * HL + hl) * KV4_DIM + d));
+      store_out(out + ((size_t)row * H + h) * KV4_DIM + d, acc, 1.f);
     }
   } else {
     for (int x = tid; x < H * (KV4_DIM / 4); x += A4_THREADS) {
@@ -858,17 +900,11 @@ attn_kv4_split_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict_
         inv[mt][r] = wl[16 * mt + g + 8 * r];
       }
     dead_heads<MT>(H, g, f, mx, inv);
-    // the partial outputs in the rings have been read, by this CTA and by the others
-    if (C > 1)
-      cl.sync();
-    else
-      __syncthreads();
+    __syncthreads();  // the partial outputs in the rings have been read
     Ring<NST, NST - 1, false> again;
     again.init(irow, e0, e1, warp, A4_WARPS, kbase, kcap, kv4, kv4_scale, mem, lane);
     weigh_again<MT>(again, lp, qf, f, mx, inv, lane, weights + kbase, status);
-    return;
   }
-  if (C > 1) cl.sync();  // no CTA leaves while another reads its shared memory
 }
 
 struct AttnArgs {

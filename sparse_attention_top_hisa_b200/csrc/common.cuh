@@ -182,6 +182,14 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int *warp_tot, int *t
   return excl;
 }
 
+// Barrier of the cluster in two halves, for all threads of its CTAs.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // Launch `func` as a programmatic dependent of the previous kernel on `st` (its
 // launch may overlap that kernel's tail; the kernel itself must execute
 // griddepcontrol.wait before touching memory).  On the legacy default stream the

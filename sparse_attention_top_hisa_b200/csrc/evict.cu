@@ -50,14 +50,6 @@ struct EvictShared {
   int any_odd;                   // of the cluster
 };
 
-// Barrier of the cluster in two halves, for all threads of its CTAs.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-
 // Warp 0: the bin, from the highest, in which the counts of the cluster's C CTAs pass `left`.
 // Two steps of one remote look each: 64 coarse bins, then the 32 bins of one of them.
 __device__ __forceinline__ void find_bin(cg::cluster_group &cl, EvictShared &sm, int C, int me,
@@ -211,7 +203,8 @@ evict_select_kernel(const long long *__restrict__ weights, const int32_t *__rest
   __shared__ EvictShared sm;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), me = (int)cl.block_rank();
-  const int s = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lc = 31 - __clz(C);  // C is a power of two
+  const int s = blockIdx.x >> lc, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int base = __ldg(cu_k + s), cap = __ldg(cu_k + s + 1) - base;
   const int len = seqlens ? __ldg(seqlens + s) : cap, budget = __ldg(keep + s);
   // these leave the whole cluster together
@@ -233,7 +226,7 @@ evict_select_kernel(const long long *__restrict__ weights, const int32_t *__rest
   const int lo = sink, hi = len - recent;
   const long long *ws = weights + base;
   // this CTA's tokens: [c0, c1), a whole number of EV_PER but for the last
-  const int chunk = ((len + C - 1) / C + EV_PER - 1) / EV_PER * EV_PER;
+  const int chunk = (((len + C - 1) >> lc) + EV_PER - 1) / EV_PER * EV_PER;
   const int c0 = min(len, me * chunk), c1 = min(len, c0 + chunk);
   const int m0 = max(c0, lo), m1 = max(m0, min(c1, hi));  // its middle tokens
   const int first = c0 + tid * EV_PER;                    // this thread's first of group 0
@@ -497,7 +490,7 @@ struct RowArrays {
 
 constexpr int ER_THREADS = 256;
 // rows of a CTA and pieces of a thread in flight (16 sequences of up to 32768 tokens with
-// their selection: 43 us with 128 and 4, 51 with 64 and 4, 52 with 256 and 8)
+// their selection: 40 us with 128 and 4, 45 with 64 and 4 or 128 and 8, 42 with 256 and 8)
 constexpr int ER_ROWS = 128, ER_UNROLL = 4;
 
 struct EvictSeq {
