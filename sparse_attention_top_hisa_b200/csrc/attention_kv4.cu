@@ -64,8 +64,8 @@ __device__ __forceinline__ int a4_chunk(int t, int chunk) {
 // What bounds it: issue.  A step of 32 tokens and 16 heads takes about 650 instructions
 // beside its 64 matrix instructions (352 of them turn 8192 nibbles into fp16), which in
 // this mix leave room for about 2.5 instructions per cycle; the gather (160 bytes of L2
-// sectors per token, 4.9 TB/s of the 17 the same copies reach alone) and DRAM are idle
-// beside it.  8192 queries x 2048 tokens x 16 heads: 550 us, 250 TFLOP/s.  Measured and
+// sectors per token, 5.0 TB/s of the 17 the same copies reach alone) and DRAM are idle
+// beside it.  8192 queries x 2048 tokens x 16 heads: 540 us, 255 TFLOP/s.  Measured and
 // left out: the value product of one step written between the scores of the next (658
 // against 637 us at the time), four CTAs per SM of 128 registers (697, spills), and the
 // same products on the tensor core that reads shared memory: it takes about 85 cycles for
@@ -186,50 +186,72 @@ __device__ __forceinline__ void convert_query(const QueryRaw<MT> &raw, float sca
 }
 
 // A lane's places in a ring stage: the swizzle of a token's row depends on the token modulo
-// 8 only, so every other token is a constant distance away.
+// 8 only, so every other token is a constant distance away.  Rows without their value half
+// (VALUES false) need no swizzle: two of them fill the banks.
+template <bool VALUES>
 struct LanePlaces {
+  static constexpr int ROW = VALUES ? KV4_ROW : KV4_HALF, CODES = A4_STEP * ROW;
+  static constexpr int STAGE = CODES + A4_STEP * KV4_NS;
   uint32_t kc, ks;        // token g: the lane's 16 key bytes, its two key scales
   uint32_t v0, v1;        // tokens 2c and 2c + 1: the lane's 8 value bytes
   uint32_t s0;            // token 2c: its value scale
   uint32_t d0, d1;        // copies: chunks lane % 4 and lane % 4 + 4 of token lane / 4
   __device__ __forceinline__ explicit LanePlaces(int lane) {
     const int g = lane >> 2, c = lane & 3, t = 2 * c;
-    kc = g * KV4_ROW + (a4_chunk(g, c) << 4);
-    ks = A4_CODES + g * KV4_NS + 2 * c;
+    kc = g * ROW + ((VALUES ? a4_chunk(g, c) : c) << 4);
+    ks = CODES + g * KV4_NS + 2 * c;
+    d0 = kc;
+    d1 = g * KV4_ROW + (a4_chunk(g, c + 4) << 4);
     v0 = t * KV4_ROW + (a4_chunk(t, 4 + (g >> 1)) << 4) + (g & 1) * 8;
     v1 = (t + 1) * KV4_ROW + (a4_chunk(t + 1, 4 + (g >> 1)) << 4) + (g & 1) * 8;
-    s0 = A4_CODES + t * KV4_NS + 8 + g;
-    d0 = g * KV4_ROW + (a4_chunk(g, c) << 4);
-    d1 = g * KV4_ROW + (a4_chunk(g, c + 4) << 4);
+    s0 = CODES + t * KV4_NS + 8 + g;
   }
 };
 
-// Raw scores of the tokens 8j .. 8j + 7 of a ring stage: s[mt] is their score fragment.
-// qs: the query fragments at this lane's place (shared address).
-template <int MT>
-__device__ __forceinline__ void kv4_scores(uint32_t stage, int j, const LanePlaces &lp,
-                                           uint32_t qs, uint32_t magic,
-                                           float (&s)[MT][4][4]) {
-  const uint4 kw = lds<uint4>(stage + lp.kc + j * 8 * KV4_ROW);
-  const uint32_t sb = lds<uint16_t>(stage + lp.ks + j * 8 * KV4_NS);
-  const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+// Raw scores of the tokens 8j0 .. 8(j0 + J) - 1 of a ring stage: s[mt] are their score
+// fragments.  qs: the query fragments at this lane's place (shared address).  J octets of
+// tokens side by side share the query's loads and give the matrix unit independent sums (8192
+// queries of 2048 tokens: 541 us by twos, 552 one by one or by fours; 32 heads, 2.5 M entries:
+// 188 us against 238, the registers being fewer too).
+template <int J, int MT, typename LP>
+__device__ __forceinline__ void kv4_scores(uint32_t stage, int j0, const LP &lp, uint32_t qs,
+                                           uint32_t magic, float (&s)[MT][4][4]) {
+  uint32_t w[J][4], sb[J];
+#pragma unroll
+  for (int j = 0; j < J; j++) {
+    const uint4 kw = lds<uint4>(stage + lp.kc + (j0 + j) * 8 * LP::ROW);
+    w[j][0] = kw.x;
+    w[j][1] = kw.y;
+    w[j][2] = kw.z;
+    w[j][3] = kw.w;
+    sb[j] = lds<uint16_t>(stage + lp.ks + (j0 + j) * 8 * KV4_NS);
+  }
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    // both halves of the scale pair: byte 0 (words 0, 1) or byte 1 (words 2, 3)
-    const __half2 sc = as_half2(__byte_perm(sb, 0u, i < 2 ? 0x4040 : 0x4141) << 7);
-    const __half2 c72 = kv4_c72(sc);
-    const uint32_t b0 = kv4_pair(w[i] << 4, magic, sc, c72), b1 = kv4_pair(w[i], magic, sc, c72);
-    const uint32_t b2 = kv4_pair(w[i] >> 4, magic, sc, c72);
-    const uint32_t b3 = kv4_pair(w[i] >> 8, magic, sc, c72);
+    uint32_t b[J][4];
+#pragma unroll
+    for (int j = 0; j < J; j++) {
+      // both halves of the scale pair: byte 0 (words 0, 1) or byte 1 (words 2, 3)
+      const __half2 sc = as_half2(__byte_perm(sb[j], 0u, i < 2 ? 0x4040 : 0x4141) << 7);
+      const __half2 c72 = kv4_c72(sc);
+      b[j][0] = kv4_pair(w[j][i] << 4, magic, sc, c72);
+      b[j][1] = kv4_pair(w[j][i], magic, sc, c72);
+      b[j][2] = kv4_pair(w[j][i] >> 4, magic, sc, c72);
+      b[j][3] = kv4_pair(w[j][i] >> 8, magic, sc, c72);
+    }
 #pragma unroll
     for (int mt = 0; mt < MT; mt++) {
       const uint4 qa = lds<uint4>(qs + (mt * 8 + 2 * i) * 512);
       const uint4 qb = lds<uint4>(qs + (mt * 8 + 2 * i + 1) * 512);
-      if (i == 0)
-        mma_f16_first(s[mt][j], qa.x, qa.y, qa.z, qa.w, b0, b1);
-      else
-        mma_f16(s[mt][j], qa.x, qa.y, qa.z, qa.w, b0, b1);
-      mma_f16(s[mt][j], qb.x, qb.y, qb.z, qb.w, b2, b3);
+#pragma unroll
+      for (int j = 0; j < J; j++)
+        if (i == 0)
+          mma_f16_first(s[mt][j0 + j], qa.x, qa.y, qa.z, qa.w, b[j][0], b[j][1]);
+        else
+          mma_f16(s[mt][j0 + j], qa.x, qa.y, qa.z, qa.w, b[j][0], b[j][1]);
+#pragma unroll
+      for (int j = 0; j < J; j++)
+        mma_f16(s[mt][j0 + j], qb.x, qb.y, qb.z, qb.w, b[j][2], b[j][3]);
     }
   }
 }
@@ -238,7 +260,7 @@ __device__ __forceinline__ void kv4_scores(uint32_t stage, int j, const LanePlac
 struct ValueRaw {
   uint2 v[4];              // nibbles of the tokens 2c, 2c + 1, 2c + 8, 2c + 9
   __half2 s0, s1, k0, k1;  // their scales in pairs, and -72 times them
-  __device__ __forceinline__ void load(uint32_t stage, int i, const LanePlaces &lp) {
+  __device__ __forceinline__ void load(uint32_t stage, int i, const LanePlaces<true> &lp) {
     uint32_t sb[4];
 #pragma unroll
     for (int u = 0; u < 4; u++) {
@@ -282,6 +304,7 @@ __device__ __forceinline__ void kv4_values(const ValueRaw &r, int i, int b,
 // VALUES: the value halves of the rows are copied too.
 template <int NST, int AHEAD, bool VALUES>
 struct Ring {
+  using LP = LanePlaces<VALUES>;
   const int32_t *irow;
   int e1, nsteps, next_e, stride;   // this lane's entry of the next step to read, up to e1
   int first_e;                      // and of the first
@@ -323,10 +346,10 @@ struct Ring {
     next_e += stride;
   }
   static __device__ __forceinline__ uint32_t after(uint32_t at) {
-    return at == (NST - 1) * A4_STAGE ? 0 : at + A4_STAGE;
+    return at == (NST - 1) * LP::STAGE ? 0 : at + LP::STAGE;
   }
   // start the copy of the next step; the valid tokens in it
-  __device__ __forceinline__ uint32_t copy(const LanePlaces &lp, int lane) {
+  __device__ __forceinline__ uint32_t copy(const LP &lp, int lane) {
     int j = next_tok;
     read();
     if (j >= kcap) {
@@ -342,30 +365,30 @@ struct Ring {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         const uint8_t *src = row_of(codes, __shfl_sync(0xffffffffu, j, 8 * i + (lane >> 2)));
-        cp_async_16(a0 + i * 8 * KV4_ROW, src);
+        cp_async_16(a0 + i * 8 * LP::ROW, src);
         if (VALUES) cp_async_16(a1 + i * 8 * KV4_ROW, src + 64);
       }
-      cp_async_16(dst + A4_CODES + lane * KV4_NS, scales + (size_t)(uint32_t)j * KV4_NS);
+      cp_async_16(dst + LP::CODES + lane * KV4_NS, scales + (size_t)(uint32_t)j * KV4_NS);
     } else if (valid) {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         const int jt = __shfl_sync(0xffffffffu, j, 8 * i + (lane >> 2));
         const uint8_t *src = row_of(codes, max(jt, 0));
-        cp_async_16_or_zero(a0 + i * 8 * KV4_ROW, src, jt >= 0);
+        cp_async_16_or_zero(a0 + i * 8 * LP::ROW, src, jt >= 0);
         if (VALUES) cp_async_16_or_zero(a1 + i * 8 * KV4_ROW, src + 64, jt >= 0);
       }
-      cp_async_16_or_zero(dst + A4_CODES + lane * KV4_NS,
+      cp_async_16_or_zero(dst + LP::CODES + lane * KV4_NS,
                           scales + (size_t)(uint32_t)max(j, 0) * KV4_NS, j >= 0);
     }
     cp_async_commit();
     return valid;
   }
-  __device__ __forceinline__ void start(const LanePlaces &lp, int lane) {
+  __device__ __forceinline__ void start(const LP &lp, int lane) {
 #pragma unroll
     for (int n = 0; n < AHEAD; n++) mask[n] = copy(lp, lane);
   }
   // start one more copy, wait for the next step; its stage and the mask of its valid tokens
-  __device__ __forceinline__ uint32_t arrive(const LanePlaces &lp, int lane, uint32_t &valid) {
+  __device__ __forceinline__ uint32_t arrive(const LP &lp, int lane, uint32_t &valid) {
     __syncwarp();  // every lane has read the stage that is filled now
     const uint32_t more = copy(lp, lane);
     valid = mask[0];
@@ -476,7 +499,7 @@ struct Running {
 
 // All steps of a warp's ring.
 template <int MT, typename R>
-__device__ __forceinline__ void attend(R &ring, const LanePlaces &lp, uint32_t qf,
+__device__ __forceinline__ void attend(R &ring, const LanePlaces<true> &lp, uint32_t qf,
                                        const float (&f)[MT][2], int lane, Running<MT> &st) {
   const float NEG = -__int_as_float(0x7f800000);
   const int c = lane & 3;
@@ -490,7 +513,7 @@ __device__ __forceinline__ void attend(R &ring, const LanePlaces &lp, uint32_t q
     if (!valid) continue;
     float x[MT][4][4];
 #pragma unroll
-    for (int j = 0; j < 4; j++) kv4_scores(stage, j, lp, qf, magic, x);
+    for (int j = 0; j < 4; j += 2) kv4_scores<2>(stage, j, lp, qf, magic, x);
     // exponents against the reference maxima; -inf where there is no token
     float top = NEG;
     float y[MT][4][4];
@@ -601,11 +624,12 @@ __device__ __forceinline__ void weigh_step(int mt, int j, const float4 &t, const
 // The weights of a warp's tokens from a second look at their keys; m, inv: the row's
 // maxima and inverse sums.
 template <int MT, typename R>
-__device__ __forceinline__ void weigh_again(R &ring, const LanePlaces &lp, uint32_t qf,
+__device__ __forceinline__ void weigh_again(R &ring, uint32_t qf,
                                             const float (&f)[MT][2], const float (&m)[MT][2],
                                             const float (&inv)[MT][2], int lane,
                                             unsigned long long *weights, int *status) {
   const uint32_t magic = kv4_magic();
+  const typename R::LP lp(lane);
   ring.start(lp, lane);
   const int32_t *entry = ring.irow + ring.first_e;
   for (int n = 0; n < ring.nsteps; n++) {
@@ -615,12 +639,14 @@ __device__ __forceinline__ void weigh_again(R &ring, const LanePlaces &lp, uint3
     const int tok = (valid >> lane) & 1u ? __ldg(entry + (size_t)n * ring.stride) : -1;
     float x[MT][4][4], v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      kv4_scores(stage, j, lp, qf, magic, x);
+    for (int j0 = 0; j0 < 4; j0 += 2) {
+      kv4_scores<2>(stage, j0, lp, qf, magic, x);
 #pragma unroll
-      for (int mt = 0; mt < MT; mt++)
-        weigh_step<MT>(mt, j, make_float4(x[mt][j][0], x[mt][j][1], x[mt][j][2], x[mt][j][3]), f,
-                       m, inv, v);
+      for (int j = j0; j < j0 + 2; j++)
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++)
+          weigh_step<MT>(mt, j, make_float4(x[mt][j][0], x[mt][j][1], x[mt][j][2], x[mt][j][3]), f,
+                         m, inv, v);
     }
     add_weights(v, tok, weights, lane, status);
   }
@@ -682,7 +708,7 @@ __device__ __forceinline__ float lse_of(float mx, float sum) {
 // hide behind the other warps of the SM and nothing is merged.
 
 // WT: with weights (a kernel of its own: what the second look needs would cost the first
-// one registers, 561 us against 639 for 8192 rows of 2048 tokens and 16 heads).
+// one registers, 561 us against 639 at the time for 8192 rows of 2048 tokens and 16 heads).
 template <int MT, bool WT>
 __global__ void __launch_bounds__(A4_THREADS, a4_ctas(MT))
 attn_kv4_rows_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict__ kv4,
@@ -702,7 +728,7 @@ attn_kv4_rows_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict__
 
   const Region rg = region_of(cu_q, cu_k, S, row, lane);
   const int kbase = rg.base, kcap = rg.tokens;
-  const LanePlaces lp(lane);
+  const LanePlaces<true> lp(lane);
   const int32_t *irow = idx + (size_t)row * topk;
   Ring<NST, NST - 1, true> ring;
   ring.init(irow, 0, topk, 0, 1, kbase, kcap, kv4, kv4_scale, mem, lane);
@@ -748,7 +774,7 @@ attn_kv4_rows_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict__
     dead_heads<MT>(H, g, f, mx, inv);
     Ring<NST, NST - 1, false> again;
     again.init(irow, 0, topk, 0, 1, kbase, kcap, kv4, kv4_scale, mem, lane);
-    weigh_again<MT>(again, lp, qf, f, mx, inv, lane, weights + kbase, status);
+    weigh_again<MT>(again, qf, f, mx, inv, lane, weights + kbase, status);
   }
 }
 
@@ -790,7 +816,7 @@ attn_kv4_split_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict_
   float *cm = wl + A4_WARPS * NH, *cs = cm + NH;  // the CTA's maximum and sum per head
   float *xm = cs + NH;                            // factors of the cluster's CTAs [NH][C]
   if (C > 1) cluster_arrive();  // this CTA runs: the others may write to it
-  const LanePlaces lp(lane);
+  const LanePlaces<true> lp(lane);
   const int e0 = me * per_cta, e1 = min(topk, e0 + per_cta);
   const int32_t *irow = idx + (size_t)row * topk;
   uint8_t *mem = a4_smem + warp * RING;
@@ -903,7 +929,7 @@ attn_kv4_split_kernel(const uint16_t *__restrict__ q, const uint8_t *__restrict_
     __syncthreads();  // the partial outputs in the rings have been read
     Ring<NST, NST - 1, false> again;
     again.init(irow, e0, e1, warp, A4_WARPS, kbase, kcap, kv4, kv4_scale, mem, lane);
-    weigh_again<MT>(again, lp, qf, f, mx, inv, lane, weights + kbase, status);
+    weigh_again<MT>(again, qf, f, mx, inv, lane, weights + kbase, status);
   }
 }
 
