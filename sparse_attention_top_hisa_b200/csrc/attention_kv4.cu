@@ -986,23 +986,40 @@ static cudaError_t launch_split(const AttnArgs &a, int C, cudaStream_t st) {
                             a.topk, per * A4_STEP, a.scale, a.out, a.lse, a.weights, a.status);
 }
 
+// CTAs of a row (1, 2, 4 or 8: a cluster) when there are few rows.  In tenths of a step (0.87 us
+// for one tile of heads, 1.23 for two): a warp's steps, slower where a second or third CTA
+// shares its SM (clusters leave some SMs of the chip's groups out), and the merge.  Measured
+// in us with 1, 2, 4 and 8 CTAs, 16 heads: 16 rows of 2048 tokens 17.8, 12.4, 8.7, 8.3; 64
+// rows 18.1, 12.4, 11.2, 17.8; 16 rows of 512 tokens 7.4, 6.8, 5.9, 6.5; 16 of 256 5.5, 6.1,
+// 5.8, 6.4; 32 heads: 64 rows of 2048 26.9, 18.1, 16.9, 22.7; 100 rows 27.1, 25.1, 30.8, 40.9.
+static int cluster_of_row(int MT, int total_q, int steps, int num_sms) {
+  int best = 1;
+  long long least = 0;
+  for (int C = 1; C <= A4_MAX_CLUSTER && total_q <= num_sms; C *= 2) {
+    const int room = C <= 2 ? num_sms : C == 4 ? num_sms * 8 / 9 : num_sms * 13 / 16;
+    const int share = (total_q * C + room - 1) / room;  // CTAs of an SM
+    if (share > a4_ctas(MT)) break;
+    const int merge = C == 1 ? 0 : C == 2 ? (MT == 1 ? 20 : 11) : (MT == 1 ? 15 : 6);
+    const long long w = (steps + A4_WARPS * C - 1) / (A4_WARPS * C);
+    const long long cost = w * (share == 1 ? 10 : share == 2 ? 16 : 25) + merge;
+    if (C > 1 && cost >= least) continue;
+    best = C;
+    least = cost;
+  }
+  return best;
+}
+
 template <int MT, bool WT>
 static cudaError_t launch_attn(const AttnArgs &a, int num_sms, cudaStream_t st) {
   const int steps = (a.topk + A4_STEP - 1) / A4_STEP;
-  // Few rows: a row is split over a CTA's warps, and over the CTAs of a cluster while that
-  // leaves SMs idle and every CTA has a step for each of its warps; up to two CTAs per SM
-  // where it saves at least two steps of each warp (64 rows of 2048 tokens and 16 heads 17.3
-  // us with 2 CTAs, 15.1 with 4; but 128 rows of 256 tokens 8.2 with 1, 10.3 with 2).
-  int C = 1;
-  while (C < A4_MAX_CLUSTER &&
-         ((a.total_q * C * 2 <= num_sms && steps >= C * 2 * A4_WARPS) ||
-          (a.total_q * C <= num_sms && steps >= C * 4 * A4_WARPS)))
-    C *= 2;
+  // Few rows: a row is split over a CTA's warps, and over the CTAs of a cluster
+  const int C = cluster_of_row(MT, a.total_q, steps, num_sms);
   // With many rows a warp has one to itself.  A row's start and end cost a warp about 2.5
   // steps, four times if four warps share it; one warp alone leaves half a row's steps idle
   // in the last wave instead of half of a quarter.  Measured (us, one warp / four): 16 heads,
-  // 2048 tokens 2400 rows 211 / 186, 8192 rows 561 / 591; 512 tokens 1200 rows 38 / 37,
-  // 2400 rows 61 / 65; two warps were never the best of the three by 5%.
+  // 2048 tokens 2400 rows 200 / 184, 4800 rows 350 / 350; 512 tokens 1200 rows 38 / 36, 2400
+  // rows 58 / 63; 128 tokens 600 rows 12.1 / 13.0; 32 heads, 2048 tokens 2400 rows 329 / 303,
+  // 4800 rows 585 / 612; two warps were never the best of the three by 5%.
   const long long slots = (long long)num_sms * a4_ctas(MT) * A4_WARPS;
   const int spared = steps - (steps + A4_WARPS - 1) / A4_WARPS;
   if (C > 1 || 15ll * a.total_q <= slots * spared) return launch_split<MT, WT>(a, C, st);
