@@ -595,3 +595,15 @@ def test_rows_behind_the_last_sequence_add_nothing(heads, topk, news):
         h.hisa_token_weights(q, k, idx, lse_pad, cu_q, cu_k, c.scale, tw)
         assert h.hisa_device_status(clear=True) == status
         assert torch.equal(tw, want_tw)
+
+
+@pytest.mark.parametrize("heads", [1, 2, 5, 7, 16, 17, 31, 32])
+@pytest.mark.parametrize("rows,topk", [(1, 2048), (3, 1000), (20, 2048), (70, 512)])
+def test_attention_rows_over_clusters(heads, rows, topk):
+    """Every number of CTAs of a row, with fewer heads than CTAs and heads that do not divide
+    among them; some rows without an index, and some whose first CTAs have none."""
+    c = Case(3 * heads + rows, heads, topk, [3000, 2500], [(rows + 1) // 2, rows // 2],
+             empty=5)
+    c.idx[0, :topk * 3 // 4] = -1
+    c.check()
+    c.check(weights=False)
