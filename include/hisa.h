@@ -393,8 +393,9 @@ hisa_status hisa_kv4_load(const uint8_t *kv4, const uint8_t *kv4_scale,
  * index >= 0 in it is one outside the region.
  * Precision: q.k are sums of exact products in fp32 (a value of q more than 2^28 times
  * smaller than its head's largest loses bits); maxima, sums, lse and weights are fp32;
- * the softmax weights enter the value product as fp16 (11 significant bits) and the
- * result is rounded once to bf16.
+ * the softmax weights enter the value product as fp16, off by at most 2^-11 of themselves
+ * or 2^-32 of the row's largest, whichever is more (so out is off by at most k * 2^-32 of the
+ * largest value besides), and the result is rounded once to bf16.
  */
 hisa_status hisa_sparse_attention_kv4(const hisa_bf16 *q_att, const uint8_t *kv4,
                                       const uint8_t *kv4_scale, const int32_t *topk_idx,

@@ -24,9 +24,12 @@
 //
 // Precision: q (bf16) is held as fp16 times a power of two per head, exact over 29 binades
 // below the head's largest value; the products are exact and summed in fp32; maxima and
-// sums are fp32; the softmax weights enter the value product as fp16 (relative error at
-// most 2^-11, an eighth of the bf16 output's own rounding), taken against a reference that
-// the maximum never exceeds by more than 2^8.
+// sums are fp32; the softmax weights enter the value product as fp16.  They are taken
+// against a reference 2^7 below a maximum that later ones pass by 2^8 at most, so that they
+// use fp16's whole range: at most 2^15, and the largest of a share at least 2^7.  A weight of
+// 2^-21 of that one and more is off by at most 2^-11 of itself (an eighth of the bf16
+// output's own rounding); a smaller one by half the smallest fp16 number, 2^-25, which is
+// 2^-32 of it.  n selected tokens are so off by at most n 2^-32 of the largest value.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -42,7 +45,9 @@ constexpr int A4_STEP = 32;                                   // tokens of a war
 constexpr int A4_CODES = A4_STEP * KV4_ROW;                   // 4096 bytes
 constexpr int A4_STAGE = A4_CODES + A4_STEP * KV4_NS;         // 4608
 constexpr int A4_MAX_CLUSTER = 8;
-constexpr float A4_TAU = 8.f;    // tolerated growth of a head's maximum, in powers of two
+// A head's reference: this many powers of two below its maximum when it was last raised, and
+// how far a score may pass the reference before it is raised again.
+constexpr float A4_BELOW = 7.f, A4_TOP = A4_BELOW + 8.f;
 constexpr int A4_OSTRIDE = KV4_DIM + 4;                       // padded row of partial outputs
 constexpr float LOG2E = 1.4426950408889634f, LOG2E_LO = 1.92596303e-8f, LN2 = 0.6931471805599453f;
 
@@ -435,7 +440,7 @@ __device__ __forceinline__ void add_weights(float (&v)[8], int tok, unsigned lon
   if (fx) atomicAdd(weights + j, fx);
 }
 
-// Factor of a share with maximum m and sum l in a merge whose maximum is mx: 0 for a share
+// Factor of a share with reference m and sum l in a merge whose largest is mx: 0 for a share
 // of no score; a share that holds a NaN keeps it whatever its maximum says.
 __device__ __forceinline__ float share_factor(float m, float l, float mx) {
   return l != l ? l : m == -__int_as_float(0x7f800000) ? 0.f : ex2(m - mx);
@@ -468,8 +473,8 @@ __device__ __forceinline__ void store_out(uint16_t *dst, const float4 &v, float 
                                                *reinterpret_cast<const uint32_t *>(&b));
 }
 
-// A warp's running state over its tokens: unnormalised outputs, reference maxima (in
-// exponents of two) and sums of its 16-head tiles.
+// A warp's running state over its tokens: unnormalised outputs, references (in exponents of
+// two) and sums of its 16-head tiles.
 template <int MT>
 struct Running {
   float o[MT][16][4];
@@ -514,7 +519,7 @@ __device__ __forceinline__ void attend(R &ring, const LanePlaces<true> &lp, uint
     float x[MT][4][4];
 #pragma unroll
     for (int j = 0; j < 4; j += 2) kv4_scores<2>(stage, j, lp, qf, magic, x);
-    // exponents against the reference maxima; -inf where there is no token
+    // exponents against the references; -inf where there is no token
     float top = NEG;
     float y[MT][4][4];
 #pragma unroll
@@ -544,14 +549,14 @@ __device__ __forceinline__ void attend(R &ring, const LanePlaces<true> &lp, uint
       for (int j = 0; j < 4; j++)
 #pragma unroll
         for (int e = 0; e < 4; e++) top = fmaxf(top, y[mt][j][e]);
-    // the reference maxima rise (and sums and outputs are rescaled) only where a score
-    // exceeds one by 2^TAU; a first score always does
-    if (__any_sync(0xffffffffu, top > A4_TAU)) {
+    // the references rise (and sums and outputs are rescaled) only where a score passes one
+    // by 2^A4_TOP; a first score always does
+    if (__any_sync(0xffffffffu, top > A4_TOP)) {
 #pragma unroll
       for (int mt = 0; mt < MT; mt++)
 #pragma unroll
         for (int r = 0; r < 2; r++) {
-          float mx = m[mt][r];
+          float mx = NEG;
 #pragma unroll
           for (int j = 0; j < 4; j++)
 #pragma unroll
@@ -559,6 +564,7 @@ __device__ __forceinline__ void attend(R &ring, const LanePlaces<true> &lp, uint
               if (y[mt][j][e] != NEG) mx = fmaxf(mx, x[mt][j][e] * f[mt][r]);
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          mx = fmaxf(m[mt][r], mx - A4_BELOW);
           const float a = mx == NEG ? 1.f : ex2(m[mt][r] - mx);
           m[mt][r] = mx;
           l[mt][r].x *= a;
@@ -622,7 +628,7 @@ __device__ __forceinline__ void weigh_step(int mt, int j, const float4 &t, const
 }
 
 // The weights of a warp's tokens from a second look at their keys; m, inv: the row's
-// maxima and inverse sums.
+// references and inverse sums.
 template <int MT, typename R>
 __device__ __forceinline__ void weigh_again(R &ring, uint32_t qf,
                                             const float (&f)[MT][2], const float (&m)[MT][2],
@@ -655,7 +661,7 @@ __device__ __forceinline__ void weigh_again(R &ring, uint32_t qf,
 
 // A warp's partial output to its ring, [head][dimension] with the 4-value pieces of a
 // 32-dimension block turned by the block so that the lanes' stores spread over the banks;
-// its maxima and sums to wm and wl.
+// its references and sums to wm and wl.
 template <int MT>
 __device__ __forceinline__ void store_share(const Running<MT> &st, uint8_t *ring, float *wm,
                                             float *wl, int lane) {
@@ -682,7 +688,7 @@ __device__ __forceinline__ void store_share(const Running<MT> &st, uint8_t *ring
     }
 }
 
-// Maxima and sums of W warps' shares of head h: their factors replace the maxima in wm.
+// References and sums of W warps' shares of head h: their factors replace the references in wm.
 template <int W>
 __device__ __forceinline__ void join_shares(float *wm, const float *wl, int NH, int h, float &mx,
                                             float &sum) {

@@ -1,0 +1,57 @@
+"""Edges of the 4-bit cache on the GPU: small softmax weights beside a large one of no value,
+rows behind the last sequence, scale bytes that the store does not write."""
+
+import numpy as np
+import pytest
+import torch
+
+import kv4_ref
+from parity import dev_i32
+from test_gpu_kv4 import DIM, H, bf16, f64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("nats", [12.0, 17.4, 19.0])
+@pytest.mark.parametrize("heads", [8, 20])
+@pytest.mark.parametrize("rows", [1, 40, 1500])
+def test_small_weights_beside_a_sink_of_no_value(nats, heads, rows):
+    """A first token whose score lies far above all others' and whose value is zero: the output
+    is the others', however small their weights are beside its own.
+
+    A weight enters the value product as fp16, taken against a reference under which the largest
+    weight of its share is at least 2^7: it is off by 2^-11 of itself or by 2^-25, half the
+    smallest fp16 number, so n of them by n 2^-32 of the largest value after the division by the
+    sum.  The rest of the tolerance is that of Attention.check_out."""
+    h = H()
+    rng = np.random.Generator(np.random.PCG64(int(nats * 10) + heads + rows))
+    length, topk, cap = 2100, 2048, 2176
+    k = np.zeros((cap, DIM))
+    k[0, 0] = 7.0  # held exactly: scale 1, q = 7
+    v = rng.uniform(1.0, 2.0, (cap, DIM))
+    v[0] = 0.0
+    codes, scales = kv4_ref.pack(*kv4_ref.quantise(k), *kv4_ref.quantise(f64(bf16(v, "cpu"))))
+    q = np.zeros((rows, heads, DIM))
+    q[:, :, 0] = 1.0
+    scale = nats / 7.0
+    picked = [rng.permutation(np.arange(1, length))[:topk - 1] for _ in range(min(rows, 40))]
+    idx = np.stack([np.insert(picked[r % len(picked)], r * 37 % topk, 0) for r in range(rows)]) \
+        .astype(np.int32)
+    lse = torch.empty(rows, heads, device="cuda")
+    w = torch.zeros(cap, dtype=torch.int64, device="cuda")
+    args = (bf16(q), torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(),
+            dev_i32(idx), dev_i32([0, rows]), dev_i32([0, cap]), scale)
+    outs = [h.hisa_sparse_attention_kv4(*args),
+            h.hisa_sparse_attention_kv4(*args, lse=lse, weights=w)]
+    kr, vr = kv4_ref.values(codes, scales)
+    n = min(rows, 40)
+    ref = kv4_ref.Attention(q[:n], kr, vr, idx[:n], [0, n], [0, cap],
+                            np.float64(np.float32(scale)))
+    rel = 2.0 ** -11 + 2 * ref.score_error() + topk * 2.0 ** -22
+    tol = 2.0 ** -8 * np.abs(ref.out) + rel[..., None] * ref.spread * (1 + 2.0 ** -8) \
+        + topk * 2.0 ** -32 * np.abs(vr).max() * (1 + 2.0 ** -7)
+    assert tol.max() < ref.out.min() / 6  # the weights of this test are within its reach
+    for out in outs:
+        err = np.abs(f64(out[:n]) - ref.out)
+        assert np.all(err <= tol), float((err / ref.out).max())
+    ref.check_lse(f64(lse[:n]))
