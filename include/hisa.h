@@ -388,7 +388,7 @@ hisa_status hisa_kv4_load(const uint8_t *kv4, const uint8_t *kv4_scale,
  *                  weight that is not a number adds nothing and raises
  *                  HISA_ERR_INVALID_ARG in the device status word.
  * Every other argument and the errors are those of hisa_sparse_attention, and total_q is
- * below 2^25 and k at most 2^28.  out must be 16-byte aligned.  A query row behind the last
+ * below 2^25 and k at most 2^20.  out must be 16-byte aligned.  A query row behind the last
  * sequence (cu_seqlens_q[num_seqs] <= row < total_q, in a padded batch) has no tokens: an
  * index >= 0 in it is one outside the region.
  * Precision: q.k are sums of exact products in fp32 (a value of q more than 2^28 times
@@ -412,7 +412,7 @@ hisa_status hisa_sparse_attention_kv4(const hisa_bf16 *q_att, const uint8_t *kv4
  *   lse            fp32 [total_q, num_heads] as hisa_sparse_attention wrote it for the same
  *                  q_att, k_att, topk_idx and scale; a head with lse -inf adds nothing.
  * Any subset of the query rows may be given (an observation window at a prompt's end);
- * rows behind the last sequence and the limits of total_q and k as above.
+ * rows behind the last sequence as above; total_q is below 2^25 and k at most 2^28.
  * A weight that is not a number, or larger than 4096, adds nothing and raises
  * HISA_ERR_INVALID_ARG in the device status word, as does an index outside the region.
  */
