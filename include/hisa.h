@@ -360,6 +360,8 @@ hisa_status hisa_sparse_attention(const hisa_bf16 *q_att, const hisa_bf16 *k_att
  *
  * Both: a sequence with an unaligned region start or inconsistent lengths is skipped (its
  * k_out and v_out rows are zeros) and reported in the device status word.
+ * Query rows behind the last sequence (cu_seqlens_q[num_seqs] <= row < total_q, in a padded
+ * batch) are no error: the store passes them over, the load writes zeros.
  */
 #define HISA_KV4_GROUP 16
 #define HISA_KV4_ROW_BYTES 128

@@ -12,13 +12,15 @@
 // decides.
 //
 // A sequence whose region or length does not fit, or with fewer live tokens than query
-// rows, is skipped whole.
+// rows, is skipped whole.  Rows behind the last sequence, in a padded batch, have no place in
+// the cache and are no error.
 //
 // One thread per group (16 per row, 8 of the key and 8 of the value): a store reads 512
 // bytes per row and writes 144, a load the reverse, so both are bound by memory (86 MB each
 // for 131072 rows; a plain copy of the card moves 6.0 TB/s at this size).  A warp takes 2
 // rows, or 4 where there are rows enough for every SM, whose loads are in flight together.
 #include <cuda_bf16.h>
+#include <limits.h>
 
 #include "kv4.cuh"
 #include "prof.cuh"
@@ -70,6 +72,7 @@ __device__ __forceinline__ void cache_rows(const int32_t *cu_q, const int32_t *c
                                            const int32_t *seqlens, int S, int row, int total_q,
                                            int *status, long long (&at)[R]) {
   const int lane = threadIdx.x & 31, first = __shfl_sync(0xffffffffu, row, 0);
+  const int rows = __ldg(cu_q + S);  // of the sequences; beside the search, not before it
   int q0 = 0, q1 = 0;
   long long base = -1;  // the cache row of query row q0, -1: the sequence is skipped
   auto look = [&](int r) {
@@ -79,7 +82,10 @@ __device__ __forceinline__ void cache_rows(const int32_t *cu_q, const int32_t *c
     const int k0 = __ldg(cu_k + s), cap = __ldg(cu_k + s + 1) - k0;
     const int len = seqlens ? __ldg(seqlens + s) : cap;
     base = (long long)k0 + len - (q1 - q0);
-    if (k0 % BLK != 0) {
+    if (r >= rows) {  // and all that come after it
+      base = -1;
+      q1 = INT_MAX;
+    } else if (k0 % BLK != 0) {
       raise_status(status, HISA_ERR_UNALIGNED);
       base = -1;
     } else if (len < 0 || len > cap || len < q1 - q0 || r < q0 || r >= q1) {

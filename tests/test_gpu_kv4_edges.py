@@ -7,7 +7,7 @@ import torch
 
 import kv4_ref
 from parity import dev_i32
-from test_gpu_kv4 import DIM, H, bf16, f64
+from test_gpu_kv4 import DIM, H, bf16, f64, hard_rows, layout, new_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,38 @@ def test_small_weights_beside_a_sink_of_no_value(nats, heads, rows):
         err = np.abs(f64(out[:n]) - ref.out)
         assert np.all(err <= tol), float((err / ref.out).max())
     ref.check_lse(f64(lse[:n]))
+
+
+@pytest.mark.parametrize("news,pad", [([1, 1, 1], 5), ([3, 0, 2], 3), ([40, 0, 1], 1),
+                                      ([0, 0, 0], 4), ([5000, 300, 7], 777)])
+def test_store_and_load_pass_over_rows_behind_the_last_sequence(news, pad):
+    """A padded batch, as the attention and the token weights take it: no error, nothing of the
+    cache touched by the padding, zeros read back for it."""
+    h = H()
+    rng = np.random.Generator(np.random.PCG64(sum(news) + pad))
+    lens = [n + 100 for n in news]
+    cu_q, cu_k = layout(lens, news)
+    n, rows = int(cu_q[-1]), int(cu_k[-1])
+    k, v = bf16(hard_rows(n + pad, rng)), bf16(hard_rows(n + pad, rng))
+    k[n:], v[n:] = float("nan"), float("inf")  # what stands in the padding is not looked at
+    kv4 = torch.full((rows, 128), 0xA5, dtype=torch.uint8, device="cuda")
+    sc = torch.full((rows, 16), 0x5A, dtype=torch.uint8, device="cuda")
+    args = dev_i32(cu_q), dev_i32(cu_k), dev_i32(lens)
+    h.hisa_device_status(clear=True)
+    h.hisa_kv4_store(k, v, *args, kv4, sc)
+    out = [torch.full((n + pad, DIM), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    h.hisa_kv4_load(kv4, sc, *args, n + pad, *out)
+    assert h.hisa_device_status(clear=True) == 0
+    codes, scales = np.zeros((0, 128), np.uint8), np.zeros((0, 16), np.uint8)
+    if n:
+        codes, scales = kv4_ref.pack(*kv4_ref.quantise(f64(k[:n])),
+                                     *kv4_ref.quantise(f64(v[:n])))
+    want = np.full((rows, 128), 0xA5, np.uint8), np.full((rows, 16), 0x5A, np.uint8)
+    at = new_rows(lens, news, cu_k)
+    want[0][at], want[1][at] = codes, scales
+    assert np.array_equal(kv4.cpu().numpy(), want[0]) and np.array_equal(sc.cpu().numpy(), want[1])
+    for got, ref in zip(out, kv4_ref.values(codes, scales)):
+        assert np.array_equal(f64(got[:n]), ref) and not got[n:].any()
+    # a sequence that does not fit is still reported, padding or not
+    h.hisa_kv4_store(k, v, args[0], args[1], dev_i32([lens[0], lens[1], rows]), kv4, sc)
+    assert h.hisa_device_status(clear=True) == (1 << 1 if news[2] else 0)
