@@ -438,6 +438,8 @@ hisa_status hisa_token_weights(const hisa_bf16 *q_att, const hisa_bf16 *k_att,
  *                  of the i-th token that stays, ascending; entries past the count are left
  *                  as they were.
  *   kept_len (out) int32 [num_seqs]: the count, min(len_s, keep[s]).
+ * Neither kept nor kept_len may overlap an input or the other (kept_len is not written over
+ * seqlens_k in one call: copy it there afterwards).
  * max_seqlen_k is at most 2^30.  A sequence with a negative budget, or with a length
  * outside its region or above max_seqlen_k, gets kept_len -1 and raises
  * HISA_ERR_INVALID_ARG in the device status word.

@@ -199,6 +199,12 @@ int num_sms() {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// whether n numbers at p and m numbers at q share memory (q may be NULL)
+bool overlap(const int32_t *p, size_t n, const int32_t *q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return q && a < b + 4 * m && b < a + 4 * n;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 hisa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? HISA_OK : HISA_ERR_CUDA; }
@@ -613,6 +619,15 @@ hisa_status hisa_evict_select(const int64_t *weights, const int32_t *cu_seqlens_
   if (!aligned(weights, 8) || !aligned(cu_seqlens_k, 4) || !aligned(seqlens_k, 4) ||
       !aligned(keep, 4) || !aligned(kept, 4) || !aligned(kept_len, 4))
     return HISA_ERR_UNALIGNED;
+  // a sequence's CTAs read its length and budget at different times, so no count may be
+  // written over one (of kept and weights only the caller knows the lengths)
+  const size_t n = (size_t)num_seqs;
+  if (overlap(kept_len, n, seqlens_k, n) || overlap(kept_len, n, keep, n) ||
+      overlap(kept_len, n, cu_seqlens_k, n + 1) || overlap(kept_len, n, kept, 1) ||
+      overlap(kept, 1, seqlens_k, n) || overlap(kept, 1, keep, n) ||
+      overlap(kept, 1, cu_seqlens_k, n + 1) ||
+      static_cast<const void *>(kept) == static_cast<const void *>(weights))
+    return HISA_ERR_INVALID_ARG;
   int *st = status_word();
   if (!st) return HISA_ERR_CUDA;
   return from_cuda(launch_evict_select(weights, cu_seqlens_k, seqlens_k, keep, num_seqs,

@@ -99,6 +99,11 @@ struct Items {  // of a Python sequence, held while they are looked at
   PyObject *operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(s, i); }
 };
 
+bool overlap(const at::Tensor &x, const at::Tensor &y) {  // of contiguous tensors
+  const uintptr_t a = (uintptr_t)x.data_ptr(), b = (uintptr_t)y.data_ptr();
+  return x.nbytes() && y.nbytes() && a < b + y.nbytes() && b < a + x.nbytes();
+}
+
 template <typename T>
 T *at_of(const at::Tensor &x) {
   return static_cast<T *>(x.data_ptr());
@@ -268,6 +273,10 @@ PyObject *evict_select(Args g) {
   kept_len = g.none(8) ? g.fresh({s}, i32) : g.tensor(8, "kept_len", at::kInt);
   if (kept.numel() != w.numel() || kept_len.numel() != s)
     bad("kept must hold one number per cache row, kept_len one per sequence");
+  for (const at::Tensor *in : {&w, &ck, &keep, lens})
+    if (in && (overlap(kept, *in) || overlap(kept_len, *in)))
+      bad("kept or kept_len overlaps an input");
+  if (overlap(kept, kept_len)) bad("kept overlaps kept_len");
   check(p_select(at_of<int64_t>(w), at_of<int32_t>(ck), n, at_of<int32_t>(keep), s, g.whole(4),
                  g.whole(5), g.whole(6), at_of<int32_t>(kept), at_of<int32_t>(kept_len),
                  g.stream),

@@ -90,3 +90,19 @@ def test_store_and_load_pass_over_rows_behind_the_last_sequence(news, pad):
     # a sequence that does not fit is still reported, padding or not
     h.hisa_kv4_store(k, v, args[0], args[1], dev_i32([lens[0], lens[1], rows]), kv4, sc)
     assert h.hisa_device_status(clear=True) == (1 << 1 if news[2] else 0)
+
+
+def test_eviction_counts_over_an_input_are_refused():
+    h = H()
+    w = torch.zeros(256, dtype=torch.int64, device="cuda")
+    cu, lens, keep = dev_i32([0, 128, 256]), dev_i32([100, 128]), dev_i32([50, 60])
+    kept, n = torch.zeros(256, dtype=torch.int32, device="cuda"), dev_i32([0, 0])
+    both = torch.zeros(258, dtype=torch.int32, device="cuda")
+    for out in (dict(kept_len=lens), dict(kept_len=keep), dict(kept_len=cu[:2]),
+                dict(kept_len=cu[1:]), dict(kept=w.view(torch.int32)[:256]),
+                dict(kept=w.view(torch.int32)[256:]), dict(kept=both[:256], kept_len=both[255:257])):
+        with pytest.raises(ValueError, match="overlaps"):
+            h.hisa_evict_select(w, cu, lens, keep, 128, 4, 4, **{**dict(kept=kept, kept_len=n), **out})
+    h.hisa_device_status(clear=True)
+    h.hisa_evict_select(w, cu, lens, keep, 128, 4, 4, kept=both[:256], kept_len=both[256:])
+    assert both[256:].tolist() == [50, 60] and h.hisa_device_status() == 0

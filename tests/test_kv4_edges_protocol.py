@@ -25,3 +25,21 @@ def test_attention_rows_too_long_for_their_precision_are_refused(lib, k):
     assert f(D, D, D, D, D, D, 1, 4, 8, k, F(0.1), D, D, D, None) == 1
     # up to the limit the call goes on to the next check
     assert f(D, D, D, D, D, D, 1, 4, 8, 1 << 20, F(0.1), ODD, D, D, None) == 2
+
+
+def test_eviction_counts_over_an_input_are_refused(lib):
+    """kept_len over seqlens_k, keep, the offsets or kept: the CTAs of a sequence read its length
+    at different times."""
+    f = lib.hisa_evict_select
+    seqs = 4
+
+    def call(weights=1 << 16, cu=2 << 16, lens=3 << 16, keep=4 << 16, kept=5 << 16, n=6 << 16,
+             most=128):
+        return f(P(weights), P(cu), P(lens) if lens else None, P(keep), seqs, most, 4, 4, P(kept),
+                 P(n), None)
+    assert call(most=-1) == 1  # the plain call is refused for other reasons only
+    for change in (dict(n=3 << 16), dict(n=4 << 16), dict(n=2 << 16), dict(n=5 << 16),
+                   dict(n=(3 << 16) + 4 * seqs - 4), dict(n=(4 << 16) - 4 * seqs + 4),
+                   dict(n=(2 << 16) + 4 * seqs), dict(kept=1 << 16), dict(kept=2 << 16),
+                   dict(kept=(3 << 16) + 4), dict(kept=4 << 16)):
+        assert call(**change) == 1, change
