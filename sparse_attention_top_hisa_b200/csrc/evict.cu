@@ -492,6 +492,9 @@ constexpr int ER_THREADS = 256;
 // rows of a CTA and pieces of a thread in flight (16 sequences of up to 32768 tokens with
 // their selection: 40 us with 128 and 4, 45 with 64 and 4 or 128 and 8, 42 with 256 and 8)
 constexpr int ER_ROWS = 128, ER_UNROLL = 4;
+// CTAs that an SM holds (48 registers), and how often they may be launched: 47360, 6 million
+// rows, which without work are gone in 30 us
+constexpr int ER_CTAS = 5, ER_WAVES = 64;
 
 struct EvictSeq {
   int sbase, dbase, scap, n;
@@ -544,30 +547,36 @@ __device__ __forceinline__ void move_rows(const uint8_t *src, uint8_t *dst, int 
   }
 }
 
+// TURNS: a sequence may have more rows than its CTAs have in one turn (code of its own: the loop
+// costs the others registers, 32.3 us against 30.4 for 16 sequences of up to 16384 rows).
+template <bool TURNS>
 __global__ void __launch_bounds__(ER_THREADS)
 evict_rows_kernel(const __grid_constant__ RowArrays a, const int32_t *__restrict__ cu_src,
                   const int32_t *__restrict__ cu_dst, const int32_t *__restrict__ kept,
                   const int32_t *__restrict__ kept_len, int max_keep, int *status) {
   __shared__ int rows[ER_ROWS];
-  const int s = blockIdx.y, r0 = blockIdx.x * ER_ROWS;
+  const int s = blockIdx.y;
   const EvictSeq q = evict_seq(cu_src, cu_dst, kept_len, s, max_keep,
                                blockIdx.x == 0 && threadIdx.x == 0, status);
-  const int n = min(ER_ROWS, q.n - r0);
-  if (n <= 0) return;
-  for (int i = threadIdx.x; i < n; i += ER_THREADS) {
-    const int from = __ldg(kept + q.sbase + r0 + i);
-    if (from < 0 || from >= q.scap) raise_status(status, HISA_ERR_INVALID_ARG);
-    rows[i] = from < 0 || from >= q.scap ? -1 : from;
-  }
-  __syncthreads();
-  for (int k = 0; k < a.n; k++) {
-    const size_t sb = (size_t)q.sbase, d = (size_t)q.dbase + r0;
-    if (a.vec[k] == 16)
-      move_rows<uint4>(a.src[k], a.dst[k], a.bytes[k] / 16, a.shift[k], rows, n, sb, d);
-    else if (a.vec[k] == 8)
-      move_rows<uint2>(a.src[k], a.dst[k], a.bytes[k] / 8, a.shift[k], rows, n, sb, d);
-    else
-      move_rows<uint32_t>(a.src[k], a.dst[k], a.bytes[k] / 4, a.shift[k], rows, n, sb, d);
+  for (uint32_t r0 = blockIdx.x * ER_ROWS; r0 < (uint32_t)q.n; r0 += gridDim.x * ER_ROWS) {
+    const int n = min(ER_ROWS, q.n - (int)r0);
+    for (int i = threadIdx.x; i < n; i += ER_THREADS) {
+      const int from = __ldg(kept + q.sbase + (size_t)r0 + i);
+      if (from < 0 || from >= q.scap) raise_status(status, HISA_ERR_INVALID_ARG);
+      rows[i] = from < 0 || from >= q.scap ? -1 : from;
+    }
+    __syncthreads();
+    for (int k = 0; k < a.n; k++) {
+      const size_t sb = (size_t)q.sbase, d = (size_t)q.dbase + r0;
+      if (a.vec[k] == 16)
+        move_rows<uint4>(a.src[k], a.dst[k], a.bytes[k] / 16, a.shift[k], rows, n, sb, d);
+      else if (a.vec[k] == 8)
+        move_rows<uint2>(a.src[k], a.dst[k], a.bytes[k] / 8, a.shift[k], rows, n, sb, d);
+      else
+        move_rows<uint32_t>(a.src[k], a.dst[k], a.bytes[k] / 4, a.shift[k], rows, n, sb, d);
+    }
+    if (!TURNS) return;
+    __syncthreads();  // the positions have been read
   }
 }
 
@@ -670,7 +679,12 @@ cudaError_t launch_evict_rows(const hisa_rows *arrays, int n, const int32_t *cu_
   }
   if (out.n > 0) {
     ProfScope ps(K_EVICT_ROWS, st);
-    evict_rows_kernel<<<dim3(max_keep / ER_ROWS + (max_keep % ER_ROWS != 0), S), ER_THREADS, 0, st>>>(
+    // max_keep is only a bound: past ER_WAVES times the CTAs that the card holds, those of a
+    // sequence take turns
+    const int want = max_keep / ER_ROWS + (max_keep % ER_ROWS != 0);
+    const int most = (ER_WAVES * ER_CTAS * num_sms + S - 1) / S;
+    const auto fn = want > most ? evict_rows_kernel<true> : evict_rows_kernel<false>;
+    fn<<<dim3(want < most ? want : most, S), ER_THREADS, 0, st>>>(
         out, cu_src, cu_dst, kept, kept_len, max_keep, status);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

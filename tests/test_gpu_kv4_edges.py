@@ -106,3 +106,42 @@ def test_eviction_counts_over_an_input_are_refused():
     h.hisa_device_status(clear=True)
     h.hisa_evict_select(w, cu, lens, keep, 128, 4, 4, kept=both[:256], kept_len=both[256:])
     assert both[256:].tolist() == [50, 60] and h.hisa_device_status() == 0
+
+
+@pytest.mark.parametrize("seqs", [1, 3, 2000, 65535])
+def test_rows_move_whatever_the_bound_of_their_count(seqs):
+    """max_keep only has to be at least every count: the launch does not grow with it (a grid of
+    65535 sequences times 2^31 rows would keep the GPU for hours).  The first sequence has more
+    rows than its CTAs have in one turn."""
+    h = H()
+    long = {1: 6200000, 3: 2100000}.get(seqs, 10000)
+    lens = np.full(seqs, 3)
+    lens[0] = long
+    keep = np.full(seqs, 2)
+    keep[0] = long - 5
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    rows = int(cu[-1])
+    kept = np.full(rows, -1, np.int32)
+    kept[cu[1:-1]], kept[cu[1:-1] + 1] = 0, 2
+    kept[:long - 5] = np.arange(5, long)
+    src = torch.arange(rows * 3, dtype=torch.int32, device="cuda").view(rows, 3)
+    dst, want = torch.zeros_like(src), np.zeros((rows, 3), np.int32)
+    host = src.cpu().numpy()
+    want[:long - 5] = host[5:long]
+    want[cu[1:-1]], want[cu[1:-1] + 1] = host[cu[1:-1]], host[cu[1:-1] + 2]
+    c, kept, n = dev_i32(cu), dev_i32(kept), dev_i32(keep)
+    h.hisa_device_status(clear=True)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    h.hisa_evict_rows([src], [dst], c, c, kept, n, long)
+    assert np.array_equal(dst.cpu().numpy(), want)
+    dst.zero_()
+    torch.cuda.synchronize()
+    start.record()
+    h.hisa_evict_rows([src], [dst], c, c, kept, n, 2 ** 31 - 1)
+    end.record()
+    torch.cuda.synchronize()
+    assert h.hisa_device_status() == 0
+    assert np.array_equal(dst.cpu().numpy(), want)
+    # 47360 CTAs, or one per sequence: well under a millisecond; 2^24 and more of them without
+    # work take several
+    assert start.elapsed_time(end) < 3
