@@ -463,7 +463,7 @@ hisa_status hisa_evict_select(const int64_t *weights, const int32_t *cu_seqlens_
  *   cu_src, cu_dst int32 [num_seqs+1] regions of the sources and of the destinations; equal
  *                  for arrays moved in place.
  *   kept, kept_len as hisa_evict_select wrote them (kept strictly ascending per sequence);
- *                  neither may be among the arrays.
+ *                  neither, nor cu_src or cu_dst, may overlap a dst.
  *   max_keep       >= every kept_len (host copy, sizes the grid); 0 launches nothing.
  * Rows past kept_len[s] of a destination region are left as they were: accumulated weights
  * moved in place keep their old numbers there, which new tokens would inherit (clear them, or

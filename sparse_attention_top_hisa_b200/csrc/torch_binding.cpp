@@ -309,8 +309,7 @@ PyObject *evict_rows(Args g) {
     const uintptr_t p = (uintptr_t)x.data_ptr();
     spans.push_back({p, p + x.nbytes(), dst});
   };
-  span(kept, false);
-  span(kept_len, false);
+  for (const at::Tensor *in : {&kept, &kept_len, &cs, &cd}) span(*in, false);
   for (Py_ssize_t i = 0; i < n; i++) {
     const at::Tensor *t[2];
     for (int d = 0; d < 2; d++) {
@@ -338,7 +337,7 @@ PyObject *evict_rows(Args g) {
   uintptr_t end = 0, end_dst = 0;
   for (const Span &x : spans) {
     if (x.from < (x.dst ? end : end_dst) && x.from < x.to)
-      bad("a destination overlaps a source or kept, or two destinations overlap");
+      bad("a destination overlaps a source, kept or an offset, or two destinations overlap");
     end = std::max(end, x.to);
     if (x.dst) end_dst = std::max(end_dst, x.to);
   }

@@ -145,3 +145,16 @@ def test_rows_move_whatever_the_bound_of_their_count(seqs):
     # 47360 CTAs, or one per sequence: well under a millisecond; 2^24 and more of them without
     # work take several
     assert start.elapsed_time(end) < 3
+
+
+def test_rows_over_the_offsets_are_refused():
+    h = H()
+    cu, other = dev_i32([0, 2]), dev_i32([0, 2])
+    kept, n, src = dev_i32([0, 1]), dev_i32([1]), dev_i32([5, 6])
+    for c, d in ((cu, other), (other, cu)):
+        with pytest.raises(ValueError, match="overlaps"):
+            h.hisa_evict_rows([src], [cu], c, d, kept, n, 1)
+    with pytest.raises(ValueError, match="overlaps"):
+        h.hisa_evict_rows([cu], [cu], cu, cu, kept, n, 1)
+    h.hisa_evict_rows([cu], [src], cu, cu, kept, n, 1)  # offsets may be read as any row
+    assert src.tolist() == [0, 6]
