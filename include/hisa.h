@@ -338,6 +338,9 @@ hisa_status hisa_sparse_attention(const hisa_bf16 *q_att, const hisa_bf16 *k_att
  *   kv4_scale  uint8 [rows_k, HISA_KV4_ROW_SCALES]: the scales of the 8 groups of
  *              HISA_KV4_GROUP dimensions of the key, then of the value.  A scale byte b is
  *              the fp16 number with the bit pattern b << 7 (5 exponent, 3 mantissa bits).
+ *              A byte is 0..198 (scales up to 896), or 255 in a group that is not a number.
+ *              Others are not of the format: what is read of such a group is never finite,
+ *              NaN in hisa_kv4_load, NaN or -infinity in the attention.
  * A value is (nibble - 8) * scale; it is exact in bf16.  The row of a token is its key row
  * (regions of cu_seqlens_k, as for the index keys).  kv4 and kv4_scale must be 16-byte
  * aligned.

@@ -30,14 +30,13 @@ namespace hisa {
 constexpr int KVS_THREADS = 128, KVS_WARPS = KVS_THREADS / 32;
 
 // e5m3 byte of amax / 7 (amax >= 0, finite, bf16), rounded to nearest even, at most 896
-// (byte 198)
 __device__ __forceinline__ uint32_t e5m3_seventh(float amax) {
   // 12 significant bits: ties of the quotient are exact again
   const uint32_t u = (__float_as_uint(amax * (1.f / 7.f)) + 0x800u) & 0xFFFFF000u;
   const float t = __uint_as_float(u);
   const uint32_t normal = ((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - ((127u - 15u) << 3);
   const uint32_t tiny = (uint32_t)__float2int_rn(t * 0x1p17f);  // multiples of 2^-17; 8 is 2^-14
-  return min(t < 0x1p-14f ? tiny : normal, 198u);
+  return min(t < 0x1p-14f ? tiny : normal, KV4_MAX_SCALE);
 }
 
 __device__ __forceinline__ float reciprocal(float s) {  // of a normal s, off by an ulp or two
@@ -147,7 +146,7 @@ kv4_store_kernel(const uint16_t *__restrict__ k_new, const uint16_t *__restrict_
       const float s = e5m3_value(byte);
       const float r = s > 0.f ? reciprocal(s) : 0.f;
       // |x / s| < 7.5 by the choice of s, but for the largest and the subnormal scales
-      if (byte < 8u || byte == 198u) {
+      if (byte < 8u || byte == KV4_MAX_SCALE) {
         c[0] = nibbles<true>(w, r);
         c[1] = nibbles<true>(w + 4, r);
       } else {
@@ -186,7 +185,7 @@ kv4_load_kernel(const uint8_t *__restrict__ kv4, const uint8_t *__restrict__ kv4
 #pragma unroll
   for (int i = 0; i < R; i++) {
     if (row + 2 * i >= total_q) continue;
-    const __nv_bfloat162 s = __float2bfloat162_rn(e5m3_value(b[i]));
+    const __nv_bfloat162 s = __float2bfloat162_rn(e5m3_value(b[i] > KV4_MAX_SCALE ? 255u : b[i]));
     uint32_t o[8];
 #pragma unroll
     for (int h = 0; h < 2; h++) {

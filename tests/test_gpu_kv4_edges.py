@@ -158,3 +158,41 @@ def test_rows_over_the_offsets_are_refused():
         h.hisa_evict_rows([cu], [cu], cu, cu, kept, n, 1)
     h.hisa_evict_rows([cu], [src], cu, cu, kept, n, 1)  # offsets may be read as any row
     assert src.tolist() == [0, 6]
+
+
+@pytest.mark.parametrize("byte", [0, 1, 8, 197, 198, 199, 200, 207, 223, 247, 248, 249, 254, 255])
+def test_scale_bytes_of_the_format_and_others(byte):
+    """A cache that something else than the store filled: up to byte 198 (896) both readers give
+    (nibble - 8) * scale, above it neither gives a finite number: NaN in the load and, where the
+    byte is 255, in the attention."""
+    h = H()
+    nib = np.tile(np.arange(16, dtype=np.uint8), 8)[None]
+    half = nib[:, 0::2] | (nib[:, 1::2] << 4)
+    for which in (0, 1):  # the scales of the key, of the value
+        codes = np.tile(np.concatenate([half, half], 1), (128, 1))
+        scales = np.full((128, 16), 0x70, np.uint8)
+        scales[5, 8 * which:8 * which + 8] = byte
+        dev = [torch.from_numpy(x).cuda() for x in (codes, scales)]
+        kb, vb = h.hisa_kv4_load(*dev, dev_i32([0, 6]), dev_i32([0, 128]), dev_i32([6]), 6)
+        ref = kv4_ref.values(codes[:6], scales[:6])
+        if byte > 198:
+            ref[which][5] = np.nan
+        assert np.array_equal(f64(kb), ref[0], equal_nan=True)
+        assert np.array_equal(f64(vb), ref[1], equal_nan=True)
+        for heads in (3, 20):
+            for rows in (1, 1000):  # over a cluster, one warp a row
+                q = np.zeros((rows, heads, DIM))
+                q[:, :, 3] = 1.0
+                lse = torch.empty(rows, heads, device="cuda")
+                out = h.hisa_sparse_attention_kv4(
+                    bf16(q), *dev, dev_i32(np.full((rows, 1), 5)), dev_i32([0, rows]),
+                    dev_i32([0, 128]), 1.0, lse=lse)
+                # one token: its value, and its score as the log-sum-exp (fp32, and 2^-16 of it)
+                got, x = f64(lse), float(ref[0][5, 3])
+                if byte > 198:
+                    none = np.isnan if byte == 255 else lambda y: ~np.isfinite(y)
+                    assert none(f64(out)).all() and (which or none(got).all())
+                else:
+                    assert np.array_equal(f64(out), np.broadcast_to(ref[1][5], out.shape))
+                if byte <= 198 or which:
+                    assert np.abs(got - x).max() <= 2.0 ** -16 * (1 + abs(x))
