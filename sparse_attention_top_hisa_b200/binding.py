@@ -478,6 +478,11 @@ def _native():
         except ImportError as e:
             raise ImportError("_hisa_torch.so is missing or was built for another torch: build it "
                               "with `python -m sparse_attention_top_hisa_b200.build`") from e
+        from .build import binding_tag
+        if getattr(mod, "BUILT_FOR", "") != binding_tag():
+            raise ImportError(f"_hisa_torch.so was built for {getattr(mod, 'BUILT_FOR', '?')}, this "
+                              f"is {binding_tag()}: build it with "
+                              "`python -m sparse_attention_top_hisa_b200.build`")
         mod.setup(_raise, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
             "hisa_kv4_store", "hisa_kv4_load", "hisa_sparse_attention_kv4", "hisa_token_weights",
             "hisa_evict_select", "hisa_evict_rows")))

@@ -22,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhisa.so")
 BINDING = os.path.join(HERE, "_hisa_torch.so")
+BINDING_STAMP = os.path.join(OUT_DIR, "_hisa_torch.stamp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -54,12 +55,28 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def binding_tag() -> str:
+    """What the binding is compiled against: it reads the fields of torch's tensors itself."""
+    import torch
+    return (f"torch {torch.__version__}, python {sys.version_info[0]}.{sys.version_info[1]}, "
+            f"c++11 abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}")
+
+
 def build_binding(force: bool = False) -> str:
-    """Compile the argument checks of the per-step entry points; returns the module's path."""
+    """Compile the argument checks of the per-step entry points; returns the module's path.  It
+    is built again when its sources, the flags or what it is compiled against have changed."""
     src, header = os.path.join(CSRC, "torch_binding.cpp"), os.path.join(ROOT, "include", "hisa.h")
     newest = max(os.path.getmtime(f) for f in (src, header))
+    flags = ["-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden"]
+    tag = binding_tag()
+    stamp = "\n".join([tag, *flags])
     if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
-        return BINDING
+        try:
+            with open(BINDING_STAMP) as f:
+                if f.read() == stamp:
+                    return BINDING
+        except OSError:
+            pass
     import torch
     base = os.path.dirname(torch.__file__)
     tmp = BINDING + f".tmp{os.getpid()}"
@@ -67,7 +84,7 @@ def build_binding(force: bool = False) -> str:
            os.path.join(base, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"],
            os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+    cmd = ["g++", *flags, f'-DHISA_BUILT_FOR="{tag}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-I{d}" for d in inc), src, "-o", tmp, "-L" + os.path.join(base, "lib"),
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
@@ -75,6 +92,9 @@ def build_binding(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    os.makedirs(OUT_DIR, exist_ok=True)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(stamp)
     return BINDING
 
 

@@ -354,6 +354,10 @@ PyObject *entry(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PyErr_Format(PyExc_TypeError, "%d arguments are wanted, got %zd", N, n);
     return nullptr;
   }
+  if (!g_raise) {
+    PyErr_SetString(PyExc_RuntimeError, "setup() has not been called");
+    return nullptr;
+  }
   HANDLE_TH_ERRORS
   try {
     Args g;
@@ -402,4 +406,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hisa_torch", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__hisa_torch(void) { return PyModule_Create(&module); }
+// BUILT_FOR: the torch and Python whose headers the code above was compiled with; the caller
+// compares before the first call.
+PyMODINIT_FUNC PyInit__hisa_torch(void) {
+  PyObject *m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "BUILT_FOR", HISA_BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -43,3 +43,48 @@ def test_eviction_counts_over_an_input_are_refused(lib):
                    dict(n=(2 << 16) + 4 * seqs), dict(kept=1 << 16), dict(kept=2 << 16),
                    dict(kept=(3 << 16) + 4), dict(kept=4 << 16)):
         assert call(**change) == 1, change
+
+
+def test_the_binding_is_built_again_for_another_torch(lib, monkeypatch):
+    """Its accessors are compiled against the installed torch: newer than its sources is not
+    enough to keep it."""
+    import subprocess
+    import types
+
+    import torch
+
+    from sparse_attention_top_hisa_b200 import build
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        return types.SimpleNamespace(returncode=1, stdout="", stderr="not run")
+    monkeypatch.setattr(subprocess, "run", run)
+    assert build.build_binding() == build.BINDING and not ran  # up to date
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    with pytest.raises(RuntimeError, match="not run"):
+        build.build_binding()
+    assert len(ran) == 1 and any("torch 0.0.0" in x for x in ran[0])
+
+
+def test_a_binding_of_another_torch_is_refused(lib, monkeypatch):
+    import torch
+
+    from sparse_attention_top_hisa_b200 import binding
+    monkeypatch.setattr(binding, "_torch_binding", None)
+    assert binding._native() is not None
+    monkeypatch.setattr(binding, "_torch_binding", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    with pytest.raises(ImportError, match="0.0.0"):
+        binding._native()
+
+
+def test_the_binding_refuses_calls_before_its_setup():
+    import subprocess
+    import sys
+
+    code = ("import importlib.util as u, torch; from sparse_attention_top_hisa_b200 import build; "
+            "s = u.spec_from_file_location('_hisa_torch', build.BINDING); m = u.module_from_spec(s); "
+            "s.loader.exec_module(m); m.kv4_store(*[None] * 8)")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 1 and "setup() has not been called" in r.stderr
