@@ -401,6 +401,9 @@ hisa_status hisa_kv4_load(const uint8_t *kv4, const uint8_t *kv4_scale,
  * the softmax weights enter the value product as fp16, off by at most 2^-11 of themselves
  * or 2^-32 of the row's largest, whichever is more (so out is off by at most k * 2^-32 of the
  * largest value besides), and the result is rounded once to bf16.
+ * The accumulated weights are normalised by sums of the same scores, so that most of what
+ * those lose cancels (measured: 6e-8 of a weight, root mean square, at scores up to 11, 8e-8
+ * at scores up to 30).
  */
 hisa_status hisa_sparse_attention_kv4(const hisa_bf16 *q_att, const uint8_t *kv4,
                                       const uint8_t *kv4_scale, const int32_t *topk_idx,
@@ -420,6 +423,9 @@ hisa_status hisa_sparse_attention_kv4(const hisa_bf16 *q_att, const uint8_t *kv4
  * rows behind the last sequence as above; total_q is below 2^25 and k at most 2^28.
  * A weight that is not a number, or larger than 4096, adds nothing and raises
  * HISA_ERR_INVALID_ARG in the device status word, as does an index outside the region.
+ * Precision: the exponent is fp32, with scale and lse held as pairs of fp32; 2^-24 of the
+ * score is added to it for what the matrix unit's sums lose on average, which is too much
+ * where they are exact (a weight is then larger by 2^-24 times its score).
  */
 hisa_status hisa_token_weights(const hisa_bf16 *q_att, const hisa_bf16 *k_att,
                                const int32_t *topk_idx, const float *lse,

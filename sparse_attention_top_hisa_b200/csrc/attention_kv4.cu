@@ -1097,7 +1097,10 @@ __device__ __forceinline__ void weigh(const float (&x)[MT][4][4], float f, float
 // sums still loses half a unit in its last place on average, 2^-25 to 2^-24 of it; f2 gives
 // 2^-24 of the score back.  Weights of 4096 rows of 32 heads, against 64 bits: 6e-7 of them
 // (root mean square) without it, most of that of one sign, 1.2e-7 with it; sums of single
-// matrix instructions instead of pairs 4e-7, and 2% slower.
+// matrix instructions instead of pairs 4e-7, and 2% slower.  Where the sums are exact (whole
+// numbers, few bits) nothing was cut off, and weights come out 2^-24 of their score, relative,
+// too large: 9e-7 at scores of up to 29.  That is what a single rounding of the score to fp32
+// may cost, and it is always in that direction.
 //
 // A warp has a row, or a part of one, to itself: its start hides behind the other warps.
 constexpr int TWB_ROW = KV4_DIM * 2, TWB_STAGE = A4_STEP * TWB_ROW;

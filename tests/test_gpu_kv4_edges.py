@@ -196,3 +196,66 @@ def test_scale_bytes_of_the_format_and_others(byte):
                     assert np.array_equal(f64(out), np.broadcast_to(ref[1][5], out.shape))
                 if byte <= 198 or which:
                     assert np.abs(got - x).max() <= 2.0 ** -16 * (1 + abs(x))
+
+
+def given_lse_run(q, k, idx, lse, scale):
+    """hisa_token_weights of one sequence: the weights of every cache row, as numbers."""
+    h = H()
+    rows = len(k)
+    w = torch.zeros(rows, dtype=torch.int64, device="cuda")
+    h.hisa_device_status(clear=True)
+    h.hisa_token_weights(bf16(q), bf16(k), dev_i32(idx), torch.from_numpy(lse).cuda(),
+                         dev_i32([0, len(q)]), dev_i32([0, rows]), scale, w)
+    assert h.hisa_device_status() == 0
+    return w.cpu().numpy() * 2.0 ** -32
+
+
+@pytest.mark.parametrize("heads", [1, 20])
+def test_token_weights_of_exact_sums_against_a_given_lse(heads):
+    """Whole numbers, whose products the matrix unit sums exactly, at scores of about 215: here
+    the rounding of one fp32 scale or log-sum-exp would move a weight by up to 1e-5, and the
+    2^-24 of the score that is added for what the unit cuts off elsewhere does so, which the
+    reference adds too.
+
+    Left: the exponent e is rounded twice (2^-24 of it each), 2^e is off by 2^-22, a lane adds up
+    to 4 heads and 8 lanes their sums (7 additions), half a unit of 2^-32."""
+    rng = np.random.Generator(np.random.PCG64(heads))
+    n, topk = 24, 40
+    k = rng.integers(-2, 3, (n * topk, DIM)).astype(float)
+    q = rng.integers(-2, 3, (n, heads, DIM)).astype(float)
+    k[:, :64], q[:, :, :64] = 7.0, 7.0
+    q[:, :, 0] = rng.integers(0, 8, (n, 1))
+    idx = np.stack([rng.permutation(topk) + r * topk for r in range(n)]).astype(np.int32)
+    scale = np.float32(0.0687)
+    s = np.einsum("nhd,ntd->nht", q, k[idx]) * np.float64(scale)
+    lse = (np.log(np.exp(s - 200).sum(-1)) + 200).astype(np.float32)
+    p = np.exp(s - lse.astype(np.float64)[..., None])
+    biased = p * np.exp(s * 2.0 ** -24)
+    ref = np.zeros(len(k))
+    ref[idx.ravel()] = biased.sum(1).ravel()
+    got = given_lse_run(q, k, idx, lse, float(scale))
+    e = np.abs(np.log2(p)).max()
+    assert e < 16
+    tol = ref * (2 * np.log(2) * 16 * 2.0 ** -24 + 2.0 ** -22 + 7 * 2.0 ** -24) + 2.0 ** -33
+    err = np.abs(got - ref)
+    assert np.all(err <= tol), float((err / ref).max())
+
+
+@pytest.mark.parametrize("heads", [16, 32])
+def test_token_weights_of_rounded_sums_have_no_bias(heads):
+    """Random rows: what the matrix unit cuts off lowers every score.  2^-24 of the score is added
+    for it; unless that takes more than half of the bias away it is the wrong number."""
+    rng = np.random.Generator(np.random.PCG64(heads))
+    n, topk = 64, 256
+    k = bf16(rng.standard_normal((n * topk, DIM)), "cpu").double().numpy()
+    q = bf16(2 * rng.standard_normal((n, heads, DIM)), "cpu").double().numpy()
+    idx = np.arange(n * topk, dtype=np.int32).reshape(n, topk)
+    scale = np.float32(DIM ** -0.5)
+    s = np.einsum("nhd,ntd->nht", q, k.reshape(n, topk, DIM)) * np.float64(scale)
+    lse = np.log(np.exp(s).sum(-1)).astype(np.float32)
+    p = np.exp(s - lse.astype(np.float64)[..., None])
+    got = given_lse_run(q, k, idx, lse, float(scale))
+    added = (p * s).sum() * 2.0 ** -24  # by the correction, over all weights
+    assert added > 4 * len(k) * 2.0 ** -33  # far above the accumulators' half units
+    bias = got.sum() - p.sum()
+    assert abs(bias) <= added / 2 + len(k) * 2.0 ** -33, bias / p.sum()
