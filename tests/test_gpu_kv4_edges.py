@@ -259,3 +259,112 @@ def test_token_weights_of_rounded_sums_have_no_bias(heads):
     assert added > 4 * len(k) * 2.0 ** -33  # far above the accumulators' half units
     bias = got.sum() - p.sum()
     assert abs(bias) <= added / 2 + len(k) * 2.0 ** -33, bias / p.sum()
+
+
+def test_a_padded_decode_step_in_a_graph():
+    """A step of fixed size, captured once: the sequences that take part, and their number of
+    rows, change from replay to replay, the rest of the rows is padding."""
+    h = H()
+    rng = np.random.Generator(np.random.PCG64(4))
+    lens, heads, topk, size = [700, 300, 500, 150], 12, 96, 6
+    cap = np.array([(n // 128 + 2) * 128 for n in lens])
+    cu_k = np.concatenate([[0], np.cumsum(cap)]).astype(np.int32)
+    rows = int(cu_k[-1])
+    ck, ln, cq = dev_i32(cu_k), dev_i32(lens), dev_i32([0] * 5)
+    codes, scales = kv4_ref.pack(*kv4_ref.quantise(rng.standard_normal((rows, DIM))),
+                                 *kv4_ref.quantise(rng.standard_normal((rows, DIM))))
+    kv4, sc = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    k, v = (torch.zeros(size, DIM, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.zeros(size, heads, DIM, dtype=torch.bfloat16, device="cuda")
+    idx = torch.full((size, topk), -1, dtype=torch.int32, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(size, heads, device="cuda")
+    w = torch.zeros(rows, dtype=torch.int64, device="cuda")
+
+    def step():
+        h.hisa_kv4_store(k, v, cq, ck, ln, kv4, sc)
+        h.hisa_sparse_attention_kv4(q, kv4, sc, idx, cq, ck, 0.09, out=out, lse=lse, weights=w)
+    h.hisa_device_status(clear=True)
+    step()
+    assert h.hisa_device_status() == 0  # no sequence has a row: all of it is padding
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for news in ([1, 1, 1, 1], [0, 1, 0, 1], [2, 0, 0, 0], [0, 0, 0, 0], [1, 2, 3, 0]):
+        cu_q = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+        n = int(cu_q[-1])
+        hk, hv = (rng.standard_normal((size, DIM)) for _ in range(2))
+        hi = np.full((size, topk), -1, np.int32)
+        for s in range(4):
+            for r in range(int(cu_q[s]), int(cu_q[s + 1])):
+                hi[r] = rng.permutation(lens[s])[:topk]
+        q.copy_(bf16(rng.standard_normal((size, heads, DIM))))
+        k.copy_(bf16(hk))
+        v.copy_(bf16(hv))
+        idx.copy_(torch.from_numpy(hi))
+        cq.copy_(torch.from_numpy(cu_q))
+        w.zero_()
+        out.fill_(7.0)
+        g.replay()
+        assert h.hisa_device_status() == 0
+        if n:
+            at = new_rows(lens, news, cu_k)
+            codes[at], scales[at] = kv4_ref.pack(*kv4_ref.quantise(f64(k[:n])),
+                                                 *kv4_ref.quantise(f64(v[:n])))
+        assert np.array_equal(kv4.cpu().numpy(), codes)
+        assert np.array_equal(sc.cpu().numpy(), scales)
+        if n:
+            kr, vr = kv4_ref.values(codes, scales)
+            ref = kv4_ref.Attention(f64(q[:n]), kr, vr, hi[:n], cu_q, cu_k,
+                                    np.float64(np.float32(0.09)))
+            ref.check_out(f64(out[:n]), np.abs(vr).max())
+            ref.check_lse(f64(lse[:n]))
+            ref.check_weights(w.cpu().numpy(), rows)
+        else:
+            assert not w.any()
+        assert not out[n:].any() and torch.isneginf(lse[n:]).all()
+
+
+def test_a_named_stream_and_no_lengths():
+    """Every call on a stream that is named, with the outputs made by the call; without
+    seqlens_k the regions are full."""
+    h = H()
+    rng = np.random.Generator(np.random.PCG64(12))
+    cu_q, cu_k, heads = [0, 256, 260], [0, 256, 640], 5
+    n, rows = 260, 640
+    k, v = bf16(rng.standard_normal((n, DIM))), bf16(rng.standard_normal((n, DIM)))
+    q = bf16(rng.standard_normal((n, heads, DIM)))
+    hi = np.stack([rng.permutation(256)[:40] for _ in range(n)]).astype(np.int32)
+    hw = rng.integers(0, 1 << 40, rows)
+    cq, ck, idx, keep = dev_i32(cu_q), dev_i32(cu_k), dev_i32(hi), dev_i32([100, 384])
+    for s in (torch.cuda.Stream(), torch.cuda.default_stream()):
+        kv4 = torch.zeros(rows, 128, dtype=torch.uint8, device="cuda")
+        sc = torch.zeros(rows, 16, dtype=torch.uint8, device="cuda")
+        w, w2 = torch.from_numpy(hw).cuda(), torch.zeros(rows, dtype=torch.int64, device="cuda")
+        lse = torch.empty(n, heads, device="cuda")
+        torch.cuda.synchronize()
+        h.hisa_kv4_store(k, v, cq, ck, None, kv4, sc, stream=s)
+        kb, vb = h.hisa_kv4_load(kv4, sc, cq, ck, None, n, stream=s)
+        out = h.hisa_sparse_attention_kv4(q, kv4, sc, idx, cq, ck, 0.1, lse=lse, stream=s)
+        keys = torch.zeros(rows, DIM, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        h.hisa_token_weights(q, keys, idx, lse, cq, ck, 0.0, w2, stream=s)
+        kept, kept_len = h.hisa_evict_select(w, ck, None, keep, 384, 3, 9, stream=s)
+        h.hisa_evict_rows([kv4, w], [kv4, w], ck, ck, kept, kept_len, 384, stream=s)
+        s.synchronize()
+        at = np.concatenate([np.arange(256), np.arange(636, 640)])
+        codes, scales = np.zeros((rows, 128), np.uint8), np.zeros((rows, 16), np.uint8)
+        codes[at], scales[at] = kv4_ref.pack(*kv4_ref.quantise(f64(k)), *kv4_ref.quantise(f64(v)))
+        kr, vr = kv4_ref.values(codes, scales)
+        assert np.array_equal(f64(kb), kr[at]) and np.array_equal(f64(vb), vr[at])
+        ref = kv4_ref.Attention(f64(q), kr, vr, hi, cu_q, cu_k, np.float64(np.float32(0.1)))
+        ref.check_out(f64(out), np.abs(vr).max())
+        ref.check_lse(f64(lse))
+        total = np.exp(-f64(lse)).sum() * hi.shape[1]  # scores of nothing: exp(0 - lse)
+        assert abs(float(w2.sum()) * 2.0 ** -32 - total) <= 1e-5 * total
+        stay = kv4_ref.evict_select(hw[:256], 256, 100, 3, 9)
+        assert kept_len.tolist() == [100, 384]
+        assert np.array_equal(kept[:100].cpu().numpy(), stay)
+        assert np.array_equal(kept[256:640].cpu().numpy(), np.arange(384))
+        assert np.array_equal(kv4[:100].cpu().numpy(), codes[stay])
+        assert np.array_equal(w[:100].cpu().numpy(), hw[stay])
+        assert np.array_equal(kv4[100:].cpu().numpy(), codes[100:])
