@@ -350,7 +350,9 @@ hisa_status hisa_sparse_attention(const hisa_bf16 *q_att, const hisa_bf16 *k_att
  *                  the last q_len_s positions of every sequence: a whole prompt, a chunk of
  *                  it, or the one token of a decode step.  The lengths count these tokens
  *                  already (call it after hisa_append_keys or hisa_decode_step, which
- *                  advance them); nothing else of the cache is touched.
+ *                  advance them); nothing else of the cache is touched.  Where the append
+ *                  was refused (HISA_ERR_CAPACITY: the region is full) the lengths still end
+ *                  with the token before, whose row this call then overwrites.
  * Per group of 16 dimensions with a = max |x|: scale = a / 7 rounded to nearest even (8-bit
  * unsigned, 4 significant bits), at most 896; q = x / scale rounded to nearest even and
  * clamped to -7..7.  An error is thus at most half a scale, except where |x| > 6720 or in

@@ -66,16 +66,18 @@ __device__ __forceinline__ int a4_chunk(int t, int chunk) {
   return chunk ^ (((t >> 1) & 3) << 1) ^ ((t & 1) << 2);
 }
 
-// What bounds it: issue.  A step of 32 tokens and 16 heads takes about 650 instructions
-// beside its 64 matrix instructions (352 of them turn 8192 nibbles into fp16), which in
-// this mix leave room for about 2.5 instructions per cycle; the gather (160 bytes of L2
-// sectors per token, 5.0 TB/s of the 17 the same copies reach alone) and DRAM are idle
-// beside it.  8192 queries x 2048 tokens x 16 heads: 540 us, 255 TFLOP/s.  Measured and
-// left out: the value product of one step written between the scores of the next (658
+// What bounds it: no unit alone.  A step of 32 tokens and 16 heads takes about 645
+// instructions, its 64 matrix instructions among them (352 turn 8192 nibbles into fp16), on
+// three warps per scheduler: issue slots are 58% full, ALU and matrix pipe 47% and 45%, and the
+// warps wait for a pipe, for the instruction before or for dispatch.  The gather (160 bytes of
+// L2 sectors per token, 5.0 TB/s of the 17 the same copies reach alone) and DRAM are idle
+// beside it.  8192 queries x 2048 tokens x 16 heads: 537 us, 256 TFLOP/s; 4096 queries of 32
+// heads: 454 us, 302 TFLOP/s (two warps per scheduler, matrix pipe 54%).  Measured and left
+// out: the value product of one step written between the scores of the next (658
 // against 637 us at the time), four CTAs per SM of 128 registers (697, spills), and the
-// same products on the tensor core that reads shared memory: it takes about 85 cycles for
-// each 128 tokens x 16 dimensions whatever the number of heads up to 32, so the scores alone
-// would cost 170 cycles of a step's 290.
+// same products on the tensor core that reads shared memory, with the tokens as its rows: it
+// takes about 85 cycles for each 128 tokens x 16 dimensions whatever the number of heads up
+// to 32, so the scores alone would cost 170 cycles of a step's 290.
 
 // 16 bytes global -> shared; zeros when !ok
 __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *src, bool ok) {
